@@ -21,6 +21,8 @@
 #include "kvouter.cuh"
 #include "merge.cuh"
 #include "decode.cuh"
+#include "paged.cuh"
+#include "rotate.cuh"
 #include "topk.cuh"
 
 using namespace msa;
@@ -186,12 +188,13 @@ msa_status_t set_smem(K kernel, int bytes) {
 // ------------------------------- per-kernel timing -------------------------------
 enum ProfKind {
   kPIndex, kPTopkPrefill, kPCsrCount, kPCsrScan, kPCsrOffsets, kPCsrScatter, kPCsrItems, kPKvOuter, kPMerge,
-  kPDecodeScan, kPTopkDecode, kPDecodeAttn, kPIndexTopk, kPKl, kPKlMerge, kPNumKinds
+  kPDecodeScan, kPTopkDecode, kPDecodeAttn, kPIndexTopk, kPKl, kPKlMerge,
+  kPRotate, kPPagedScan, kPPagedTopk, kPPagedAttn, kPNumKinds
 };
 const char* const kProfNames[kPNumKinds] = {"index_blockmax", "topk_prefill", "csr_count", "csr_scan",
                                             "csr_offsets", "csr_scatter", "csr_items", "kvouter", "merge",
                                             "decode_scan", "topk_decode", "decode_attn", "index_topk", "kl",
-                                            "kl_merge"};
+                                            "kl_merge", "rotate", "paged_scan", "paged_topk", "paged_attn"};
 struct ProfRec {
   int kind;
   cudaEvent_t a, b;
@@ -1116,6 +1119,8 @@ msa_status_t check_kl_params(const msa_params* p) {
   return MSA_OK;
 }
 
+#include "serving.cuh"
+
 }  // namespace
 
 // =====================================================================================
@@ -1417,6 +1422,127 @@ msa_status_t msa_index_kl(const msa_params* p, const void* q, const void* k, con
   const size_t need = msa_index_kl_workspace(p);
   if (workspace_bytes < need) return fail(MSA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
   return run_index_kl(p, q, k, q_idx, k_idx, block_ids, lse, idx_scale, kl, workspace, static_cast<cudaStream_t>(stream));
+}
+
+msa_status_t msa_rope(const msa_rope_params* p, const msa_rope_tensor* tensors, int32_t count, int64_t n, void* stream) {
+  g_detail[0] = 0;
+  msa_status_t s;
+  if (!p || !tensors) return fail(MSA_ERR_INVALID_ARG, "%s is NULL", p ? "tensors" : "params");
+  if (count < 1 || count > 4) return fail(MSA_ERR_INVALID_ARG, "count=%d out of range [1, 4]", count);
+  if (n < 0 || n > kMaxN) return fail(MSA_ERR_INVALID_ARG, "n=%lld out of range [0, %lld]", (long long)n, (long long)kMaxN);
+  if ((s = check_dtype(p->dtype)) != MSA_OK || (s = check_rope_frequencies(p->freqs, p->rot, "freqs")) != MSA_OK) return s;
+  if (!std::isfinite(p->scale)) return fail(MSA_ERR_INVALID_ARG, "scale must be finite");
+  for (int i = 0; i < count; ++i) {
+    static const char* const names[4] = {"tensor 0", "tensor 1", "tensor 2", "tensor 3"};
+    if ((s = check_rotate_tensor(tensors[i], p->dtype, p->dtype, p->rot, n, names[i])) != MSA_OK) return s;
+  }
+  if (n == 0) return MSA_OK;
+  if (p->positions == nullptr) return fail(MSA_ERR_INVALID_ARG, "positions is NULL");
+  if (reinterpret_cast<uintptr_t>(p->positions) % (p->positions_i64 ? 8 : 4) != 0)
+    return fail(MSA_ERR_INVALID_ARG, "positions is not aligned to its element");
+  RotateParams P{};
+  for (int i = 0; i < count; ++i) P.jobs[i] = rotate_job(tensors[i], p->freqs, p->rot);
+  P.count = count;
+  P.interleaved = p->interleaved != 0;
+  P.scale = p->scale;
+  P.sign = p->backward ? -1.0f : 1.0f;
+  P.n = n;
+  P.positions = p->positions;
+  P.positions_i64 = p->positions_i64 != 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (p->dtype) {
+    case MSA_BF16: return launch_rotate<__nv_bfloat16, __nv_bfloat16>(P, st);
+    case MSA_FP16: return launch_rotate<__half, __half>(P, st);
+    default: return launch_rotate<float, float>(P, st);
+  }
+}
+
+msa_status_t msa_paged_append(const msa_paged_cache* c, const msa_paged_append_params* p, const msa_rope_tensor* k,
+                              const msa_rope_tensor* v, const msa_rope_tensor* k_idx, const msa_rope_tensor* q,
+                              const msa_rope_tensor* q_idx, int64_t n, void* stream) {
+  g_detail[0] = 0;
+  msa_status_t s;
+  if (!p || !k || !v || !k_idx) return fail(MSA_ERR_INVALID_ARG, "%s is NULL", !p ? "params" : !k ? "k" : !v ? "v" : "k_idx");
+  if ((s = check_paged_cache(c)) != MSA_OK) return s;
+  if (n < 0 || n > kMaxN) return fail(MSA_ERR_INVALID_ARG, "n=%lld out of range [0, %lld]", (long long)n, (long long)kMaxN);
+  if ((s = check_dtype(p->dtype)) != MSA_OK) return s;
+  if ((s = check_sequences(c, p->batch, p->max_pages, p->table_stride, p->page_table, p->seqlens)) != MSA_OK) return s;
+  if (p->cu_seqlens == nullptr && n % p->batch != 0)
+    return fail(MSA_ERR_INVALID_ARG, "n=%lld is not a multiple of batch=%d (give cu_seqlens)", (long long)n, p->batch);
+  if (reinterpret_cast<uintptr_t>(p->cu_seqlens) % 4 != 0) return fail(MSA_ERR_INVALID_ARG, "cu_seqlens is not 4-byte aligned");
+  if (!std::isfinite(p->scale)) return fail(MSA_ERR_INVALID_ARG, "scale must be finite");
+  if (p->freqs && (s = check_rope_frequencies(p->freqs, p->rot, "freqs")) != MSA_OK) return s;
+  if (p->idx_freqs && (s = check_rope_frequencies(p->idx_freqs, p->idx_rot, "idx_freqs")) != MSA_OK) return s;
+  const int rot = p->freqs ? p->rot : 0, idx_rot = p->idx_freqs ? p->idx_rot : 0;
+  RotateParams P{};
+  // the cache's tensors: their destination is the pages
+  const struct { const msa_rope_tensor* t; void* pages; int64_t stride; int dim, rot; const double* f; const char* name; } in[3] = {
+      {k, c->k, c->k_page_stride, c->d, rot, p->freqs, "k"},
+      {v, c->v, c->v_page_stride, c->d, 0, nullptr, "v"},
+      {k_idx, c->k_idx, c->k_idx_page_stride, c->d_idx, idx_rot, p->idx_freqs, "k_idx"}};
+  for (auto& x : in) {
+    msa_rope_tensor t = *x.t;
+    if (t.heads != c->g || t.dim != x.dim)
+      return fail(MSA_ERR_INVALID_ARG, "%s: %d heads of %d, the cache has %d of %d", x.name, t.heads, t.dim, c->g, x.dim);
+    t.y = x.pages;
+    t.y_token_stride = int64_t(c->g) * x.dim;
+    t.y_head_stride = x.dim;
+    if ((s = check_rotate_tensor(t, p->dtype, MSA_BF16, x.rot, n, x.name)) != MSA_OK) return s;
+    RotateJob j = rotate_job(t, x.f, x.rot);
+    j.paged = 1;
+    j.dst_page = x.stride;
+    P.jobs[P.count++] = j;
+  }
+  const struct { const msa_rope_tensor* t; int rot; const double* f; const char* name; } out[2] = {
+      {q, rot, p->freqs, "q"}, {q_idx, idx_rot, p->idx_freqs, "q_idx"}};
+  for (auto& x : out) {
+    if (!x.t) continue;
+    if ((s = check_rotate_tensor(*x.t, p->dtype, MSA_BF16, x.rot, n, x.name)) != MSA_OK) return s;
+    P.jobs[P.count++] = rotate_job(*x.t, x.f, x.rot);
+  }
+  if (n == 0) return MSA_OK;
+  P.interleaved = p->interleaved != 0;
+  P.scale = p->scale;
+  P.sign = 1.0f;
+  P.n = n;
+  P.cu_seqlens = p->cu_seqlens;
+  P.seqlens = p->seqlens;
+  P.page_table = p->page_table;
+  P.table_stride = p->table_stride;
+  P.num_pages = c->num_pages;
+  P.batch = p->batch;
+  P.max_pages = p->max_pages;
+  P.page_shift = page_shift(c->page_size);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (p->dtype) {
+    case MSA_BF16: return launch_rotate<__nv_bfloat16, __nv_bfloat16>(P, st);
+    case MSA_FP16: return launch_rotate<__half, __nv_bfloat16>(P, st);
+    default: return launch_rotate<float, __nv_bfloat16>(P, st);
+  }
+}
+
+size_t msa_paged_decode_workspace(const msa_paged_cache* c, const msa_paged_decode_params* p) {
+  if (check_paged_shapes(c, p) != MSA_OK) return 0;
+  return paged_layout(nullptr, c, p).bytes;
+}
+
+msa_status_t msa_paged_decode(const msa_paged_cache* c, const msa_paged_decode_params* p, const void* q, const void* q_idx,
+                              int32_t* block_ids_out, void* o, void* workspace, size_t workspace_bytes, void* stream) {
+  g_detail[0] = 0;
+  msa_status_t s;
+  if ((s = check_paged_shapes(c, p)) != MSA_OK) return s;
+  if ((s = check_sequences(c, p->batch, p->max_pages, p->table_stride, p->page_table, p->seqlens)) != MSA_OK) return s;
+  if (p->n_prefix_pages < 0 || p->n_prefix_pages > p->max_pages)
+    return fail(MSA_ERR_INVALID_ARG, "n_prefix_pages=%d out of range [0, max_pages=%d]", p->n_prefix_pages, p->max_pages);
+  if (p->n_prefix_pages > 0 && (p->prefix_pages == nullptr || reinterpret_cast<uintptr_t>(p->prefix_pages) % 4 != 0))
+    return fail(MSA_ERR_INVALID_ARG, "prefix_pages is NULL or not 4-byte aligned");
+  if ((s = check_ptr(q, "q")) != MSA_OK || (s = check_ptr(q_idx, "q_idx")) != MSA_OK || (s = check_ptr(o, "o")) != MSA_OK ||
+      (s = check_ptr(workspace, "workspace")) != MSA_OK)
+    return s;
+  if (reinterpret_cast<uintptr_t>(block_ids_out) % 4 != 0) return fail(MSA_ERR_INVALID_ARG, "block_ids_out is not 4-byte aligned");
+  const size_t need = paged_layout(nullptr, c, p).bytes;
+  if (workspace_bytes < need) return fail(MSA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  return run_paged_decode(c, p, q, q_idx, block_ids_out, o, workspace, static_cast<cudaStream_t>(stream));
 }
 
 msa_status_t msa_profile_start(void) {

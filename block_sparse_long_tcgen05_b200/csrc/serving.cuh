@@ -1,0 +1,248 @@
+// Host side of the serving entry points (rotary positions, paged append, paged decode): their
+// argument checks, workspace layout and launches. Included by msa_api.cu after its helpers.
+#pragma once
+
+// ------------------------------- rotary positions, append -------------------------------
+msa_status_t check_rope_frequencies(const double* freqs, int32_t rot, const char* name) {
+  if (freqs == nullptr) return fail(MSA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(freqs) % 8 != 0) return fail(MSA_ERR_INVALID_ARG, "%s is not 8-byte aligned", name);
+  if (rot < 2 || rot % 2 != 0) return fail(MSA_ERR_INVALID_ARG, "%d rotated elements: a positive even number is wanted", rot);
+  return MSA_OK;
+}
+
+int dtype_bytes(int32_t dtype) { return dtype == MSA_FP32 ? 4 : 2; }
+
+// (n: tokens; the addresses of none do not matter)
+msa_status_t check_rotate_tensor(const msa_rope_tensor& t, int32_t dtype, int32_t out_dtype, int32_t rot, int64_t n,
+                                 const char* name) {
+  if (t.heads < 1 || t.heads > 1024) return fail(MSA_ERR_INVALID_ARG, "%s: %d heads out of range [1, 1024]", name, t.heads);
+  if (t.dim < 2 || t.dim > 1024 || t.dim % 2 != 0)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: dim=%d unsupported (even, 2..1024)", name, t.dim);
+  if (rot > t.dim) return fail(MSA_ERR_INVALID_ARG, "%s: %d rotated elements of a head of %d", name, rot, t.dim);
+  if (n == 0) return MSA_OK;
+  if (t.x == nullptr || t.y == nullptr) return fail(MSA_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (reinterpret_cast<uintptr_t>(t.x) % dtype_bytes(dtype) != 0 || reinterpret_cast<uintptr_t>(t.y) % dtype_bytes(out_dtype) != 0)
+    return fail(MSA_ERR_INVALID_ARG, "%s is not aligned to its element", name);
+  return MSA_OK;
+}
+
+RotateJob rotate_job(const msa_rope_tensor& t, const double* freqs, int32_t rot) {
+  RotateJob j{};
+  j.src = t.x;
+  j.dst = t.y;
+  j.src_token = t.x_token_stride;
+  j.src_head = t.x_head_stride;
+  j.dst_token = t.y_token_stride;
+  j.dst_head = t.y_head_stride;
+  j.freqs = freqs;
+  j.heads = t.heads;
+  j.dim = t.dim;
+  j.rot = freqs ? rot : 0;
+  return j;
+}
+
+template <typename TI, typename TO, int V>
+msa_status_t launch_rotate_v(RotateParams& P, cudaStream_t st) {
+  int64_t blocks = 0;
+  for (int i = 0; i < P.count; ++i) {
+    RotateJob& j = P.jobs[i];
+    j.head_slots = j.heads;
+    j.block0 = static_cast<unsigned int>(blocks);
+    const int64_t threads = P.n * (j.dim / (2 * V)) * j.head_slots;
+    blocks += (threads + kRotThreads - 1) / kRotThreads;
+    if (blocks > 0x7fffffff) return fail(MSA_ERR_UNSUPPORTED, "%lld tokens of %d heads are too many for one call", (long long)P.n, j.heads);
+  }
+  if (blocks == 0) return MSA_OK;
+  ProfScope ps(kPRotate, st);
+  rotate_kernel<TI, TO, V><<<unsigned(blocks), kRotThreads, 0, st>>>(P);
+  MSA_CHECK_LAUNCH();
+  return MSA_OK;
+}
+
+template <typename TI, typename TO>
+msa_status_t launch_rotate(RotateParams& P, cudaStream_t st) {
+  return launch_rotate_v<TI, TO, 1>(P, st);
+}
+
+msa_status_t check_dtype(int32_t dtype) {
+  if (dtype != MSA_BF16 && dtype != MSA_FP16 && dtype != MSA_FP32)
+    return fail(MSA_ERR_UNSUPPORTED, "dtype=%d unsupported (MSA_BF16, MSA_FP16, MSA_FP32)", dtype);
+  return MSA_OK;
+}
+
+// ------------------------------- paged cache -------------------------------
+msa_status_t check_paged_cache(const msa_paged_cache* c) {
+  if (!c) return fail(MSA_ERR_INVALID_ARG, "cache is NULL");
+  if (c->g < 1 || c->g > 64) return fail(MSA_ERR_INVALID_ARG, "g=%d out of range [1, 64]", c->g);
+  if (c->d != 64 && c->d != 128) return fail(MSA_ERR_UNSUPPORTED, "d=%d unsupported (64, 128)", c->d);
+  msa_status_t s;
+  if ((s = check_d_idx(c->d_idx)) != MSA_OK) return s;
+  const int ps = c->page_size;
+  if (ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0)
+    return fail(MSA_ERR_UNSUPPORTED, "page_size=%d unsupported (a power of two, 16..1024)", ps);
+  if (c->num_pages < 1 || c->num_pages > 0x7fffffff)
+    return fail(MSA_ERR_INVALID_ARG, "num_pages=%lld out of range [1, 2^31)", (long long)c->num_pages);
+  const struct { const void* p; int64_t stride; int dim; const char* name; } t[3] = {
+      {c->k, c->k_page_stride, c->d, "k pages"}, {c->v, c->v_page_stride, c->d, "v pages"},
+      {c->k_idx, c->k_idx_page_stride, c->d_idx, "k_idx pages"}};
+  for (auto& x : t) {
+    if ((s = check_ptr(x.p, x.name)) != MSA_OK) return s;
+    if (x.stride < int64_t(ps) * c->g * x.dim || x.stride % 8 != 0 || x.stride > (int64_t(1) << 38))
+      return fail(MSA_ERR_INVALID_ARG, "%s: page stride %lld (at least a page's elements, a multiple of 8)", x.name,
+                  (long long)x.stride);
+  }
+  return MSA_OK;
+}
+
+int page_shift(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
+msa_status_t check_sequences(const msa_paged_cache* c, int32_t batch, int32_t max_pages, int64_t table_stride,
+                             const int32_t* table, const int32_t* seqlens) {
+  if (batch < 1 || batch > kScanMaxBatch)
+    return fail(MSA_ERR_UNSUPPORTED, "batch=%d unsupported (1..%d)", batch, kScanMaxBatch);
+  if (max_pages < 1 || int64_t(max_pages) * c->page_size > kMaxN)
+    return fail(MSA_ERR_INVALID_ARG, "max_pages=%d: at least one, and at most %lld tokens", max_pages, (long long)kMaxN);
+  if (table_stride < max_pages) return fail(MSA_ERR_INVALID_ARG, "table_stride=%lld < max_pages=%d", (long long)table_stride, max_pages);
+  const struct { const void* p; const char* name; } t[2] = {{table, "page_table"}, {seqlens, "seqlens"}};
+  for (auto& x : t) {
+    if (x.p == nullptr) return fail(MSA_ERR_INVALID_ARG, "%s is NULL", x.name);
+    if (reinterpret_cast<uintptr_t>(x.p) % 4 != 0) return fail(MSA_ERR_INVALID_ARG, "%s is not 4-byte aligned", x.name);
+  }
+  return MSA_OK;
+}
+
+struct PagedLayout {
+  uint32_t* maxima = nullptr;
+  int32_t* block_ids = nullptr;
+  size_t bytes = 0;
+};
+
+int64_t paged_blocks(const msa_paged_cache* c, const msa_paged_decode_params* p) {
+  return (int64_t(p->max_pages) * c->page_size + p->bk - 1) / p->bk;
+}
+
+PagedLayout paged_layout(void* ws, const msa_paged_cache* c, const msa_paged_decode_params* p) {
+  const int64_t rows = int64_t(p->batch) * p->n_new;
+  Carver cv(ws);
+  PagedLayout L;
+  L.maxima = static_cast<uint32_t*>(cv.take(size_t(rows) * c->g * paged_blocks(c, p) * 4));
+  L.block_ids = static_cast<int32_t*>(cv.take(size_t(rows) * c->g * p->k * 4));   // used when the caller takes none
+  L.bytes = cv.off;
+  return L;
+}
+
+// Everything of a decode call but the tensors' addresses.
+msa_status_t check_paged_shapes(const msa_paged_cache* c, const msa_paged_decode_params* p) {
+  if (!c || !p) return fail(MSA_ERR_INVALID_ARG, "%s is NULL", c ? "params" : "cache");
+  msa_status_t s;
+  if (p->bk != 128 && p->bk != 64 && p->bk != 32) return fail(MSA_ERR_UNSUPPORTED, "bk=%d unsupported (32, 64, 128)", p->bk);
+  if (p->k < 1 || p->k > 32) return fail(MSA_ERR_UNSUPPORTED, "k=%d unsupported (1..32)", p->k);
+  if (p->n_new < 1 || p->n_new > 8) return fail(MSA_ERR_UNSUPPORTED, "n_new=%d unsupported (1..8 new tokens a sequence)", p->n_new);
+  if ((s = check_paged_cache(c)) != MSA_OK) return s;
+  if (p->hq < 1 || p->hq % c->g != 0) return fail(MSA_ERR_INVALID_ARG, "hq=%d is not a positive multiple of g=%d", p->hq, c->g);
+  if (p->hq / c->g > 16) return fail(MSA_ERR_UNSUPPORTED, "hq/g=%d unsupported (at most 16)", p->hq / c->g);
+  if (!(p->scale >= 0.0f) || std::isinf(p->scale)) return fail(MSA_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (p->batch < 1 || p->batch > kScanMaxBatch)
+    return fail(MSA_ERR_UNSUPPORTED, "batch=%d unsupported (1..%d)", p->batch, kScanMaxBatch);
+  if (p->max_pages < 1 || int64_t(p->max_pages) * c->page_size > kMaxN)
+    return fail(MSA_ERR_INVALID_ARG, "max_pages=%d: at least one, and at most %lld tokens", p->max_pages, (long long)kMaxN);
+  return MSA_OK;
+}
+
+template <int DI>
+msa_status_t launch_paged_scan(const PagedScanParams& P, cudaStream_t st) {
+  static std::once_flag once;
+  static int per_sm = 0;
+  std::call_once(once, [] {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_scan_kernel<DI>, kScanThreads, 0) != cudaSuccess) per_sm = 0;
+  });
+  if (per_sm < 1) return fail(MSA_ERR_CUDA, "paged scan: no resident block");
+  // at most the work of full-length sequences: eight (span, group) units a block
+  const int64_t most = int64_t(P.view.batch) * ((int64_t(P.nbmax) * P.bk + 127) / 128) * P.G;
+  const int64_t grid = std::min<int64_t>(int64_t(num_sms()) * per_sm, (most + 7) / 8);
+  ProfScope ps(kPPagedScan, st);
+  paged_scan_kernel<DI><<<unsigned(std::max<int64_t>(grid, 1)), kScanThreads, 0, st>>>(P);
+  MSA_CHECK_LAUNCH();
+  return MSA_OK;
+}
+
+template <int D>
+msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
+  using C = PagedAttnCfg<D>;
+  static std::once_flag once;
+  static msa_status_t attr = MSA_OK;
+  std::call_once(once, [] { attr = set_smem(paged_attn_kernel<D>, C::kSmemBytes); });
+  if (attr != MSA_OK) return fail(attr, "paged attention: shared memory");
+  const int64_t grid = int64_t(P.view.batch) * P.view.S * P.G;
+  ProfScope ps(kPPagedAttn, st);
+  paged_attn_kernel<D><<<unsigned(grid), kPagedAttnWarps * 32, C::kSmemBytes, st>>>(P);
+  MSA_CHECK_LAUNCH();
+  return MSA_OK;
+}
+
+msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_params* p, const void* q, const void* q_idx,
+                              int32_t* block_ids_out, void* o, void* ws, cudaStream_t st) {
+  const PagedLayout L = paged_layout(ws, c, p);
+  PageView V{};
+  V.table = p->page_table;
+  V.prefix = p->prefix_pages;
+  V.seqlens = p->seqlens;
+  V.table_stride = p->table_stride;
+  V.num_pages = c->num_pages;
+  V.prefix_pages = p->n_prefix_pages;
+  V.max_pages = p->max_pages;
+  V.shift = page_shift(c->page_size);
+  V.batch = p->batch;
+  V.S = p->n_new;
+  const int nbmax = int(paged_blocks(c, p));
+  int32_t* ids = block_ids_out ? block_ids_out : L.block_ids;
+  msa_status_t s;
+  if (p->k > 1 && nbmax > p->k) {   // else every visible block is taken, or the local one alone
+    PagedScanParams sp{};
+    sp.view = V;
+    sp.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
+    sp.pages = static_cast<const __nv_bfloat16*>(c->k_idx);
+    sp.page_stride = c->k_idx_page_stride;
+    sp.maxima = L.maxima;
+    sp.G = c->g;
+    sp.bk = p->bk;
+    sp.k = p->k;
+    sp.nbmax = nbmax;
+    sp.nb0 = 0;
+    s = c->d_idx == 128 ? launch_paged_scan<128>(sp, st) : c->d_idx == 64 ? launch_paged_scan<64>(sp, st) : launch_paged_scan<32>(sp, st);
+    if (s != MSA_OK) return s;
+  }
+  PagedTopkParams tp{};
+  tp.view = V;
+  tp.maxima = L.maxima;
+  tp.block_ids = ids;
+  tp.G = c->g;
+  tp.bk = p->bk;
+  tp.k = p->k;
+  tp.nbmax = nbmax;
+  const int64_t rg = int64_t(p->batch) * p->n_new * c->g;
+  {
+    ProfScope ps(kPPagedTopk, st);
+    paged_topk_kernel<<<unsigned((rg + 3) / 4), 128, 0, st>>>(tp);
+  }
+  MSA_CHECK_LAUNCH();
+  PagedAttnParams ap{};
+  ap.view = V;
+  ap.q = static_cast<const __nv_bfloat16*>(q);
+  ap.kp = static_cast<const __nv_bfloat16*>(c->k);
+  ap.vp = static_cast<const __nv_bfloat16*>(c->v);
+  ap.k_stride = c->k_page_stride;
+  ap.v_stride = c->v_page_stride;
+  ap.block_ids = ids;
+  ap.o = static_cast<__nv_bfloat16*>(o);
+  ap.G = c->g;
+  ap.R = p->hq / c->g;
+  ap.k = p->k;
+  ap.bk = p->bk;
+  ap.scale_log2 = (p->scale == 0.0f ? 1.0f / std::sqrt(float(c->d)) : p->scale) * 1.4426950408889634f;
+  return c->d == 128 ? launch_paged_attn<128>(ap, st) : launch_paged_attn<64>(ap, st);
+}

@@ -7,6 +7,7 @@ is missing or a call fails, these functions raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -24,7 +25,8 @@ EXPORTS = ("msa_index_select_workspace", "msa_index_select", "msa_sparse_attn_wo
            "msa_forward_workspace", "msa_forward", "msa_get_device_error", "msa_status_string",
            "msa_last_error_detail", "msa_profile_start", "msa_profile_stop", "msa_index_select_static",
            "msa_forward_host_device_bytes", "msa_forward_host", "msa_index_kl_workspace", "msa_index_kl",
-           "msa_set_wait_limit_ns")
+           "msa_set_wait_limit_ns", "msa_rope", "msa_paged_append", "msa_paged_decode_workspace",
+           "msa_paged_decode")
 
 
 class MsaError(RuntimeError):
@@ -39,6 +41,39 @@ class MsaParams(ctypes.Structure):
                 ("k", ctypes.c_int32), ("scale", ctypes.c_float), ("n", ctypes.c_int64),
                 ("lmax", ctypes.c_int64), ("seqlens", ctypes.c_void_p), ("query_chunk", ctypes.c_int64),
                 ("lse_out", ctypes.c_void_p)]
+
+
+class MsaRopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64), ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class MsaRopeParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("backward", ctypes.c_int32), ("scale", ctypes.c_float), ("positions_i64", ctypes.c_int32),
+                ("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
+class MsaPagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_idx", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64), ("k_idx_page_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("g", ctypes.c_int32), ("d", ctypes.c_int32), ("d_idx", ctypes.c_int32)]
+
+
+class MsaPagedAppendParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("rot", ctypes.c_int32), ("idx_rot", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("table_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p), ("freqs", ctypes.c_void_p),
+                ("idx_freqs", ctypes.c_void_p)]
+
+
+class MsaPagedDecodeParams(ctypes.Structure):
+    _fields_ = [("hq", ctypes.c_int32), ("batch", ctypes.c_int32), ("n_new", ctypes.c_int32), ("bk", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_prefix_pages", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("table_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p)]
 
 
 class MsaKernelStat(ctypes.Structure):
@@ -77,6 +112,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "msa_index_kl_workspace": (c_sz, [pp]),
         "msa_index_kl": (c_i32, [pp, c_p, c_p, c_p, c_p, c_p, c_p, c_f, c_p, c_p, c_sz, c_p]),
         "msa_set_wait_limit_ns": (c_i32, [ctypes.c_uint64]),
+        "msa_rope": (c_i32, [ctypes.POINTER(MsaRopeParams), ctypes.POINTER(MsaRopeTensor), c_i32, c_i64, c_p]),
+        "msa_paged_append": (c_i32, [ctypes.POINTER(MsaPagedCache), ctypes.POINTER(MsaPagedAppendParams)]
+                             + [ctypes.POINTER(MsaRopeTensor)] * 5 + [c_i64, c_p]),
+        "msa_paged_decode_workspace": (c_sz, [ctypes.POINTER(MsaPagedCache), ctypes.POINTER(MsaPagedDecodeParams)]),
+        "msa_paged_decode": (c_i32, [ctypes.POINTER(MsaPagedCache), ctypes.POINTER(MsaPagedDecodeParams), c_p, c_p, c_p,
+                                     c_p, c_p, c_sz, c_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -277,6 +318,263 @@ def decode(q, k_cache, v_cache, q_idx, k_idx_cache, seqlens, topk: int, bk: int 
     p = decode_params(B, Lmax, seqlens, Hq, G, d, d_idx, topk, bk, scale)
     return msa_forward(p, q, k_cache, v_cache, q_idx, k_idx_cache, o=o, block_ids=block_ids,
                        workspace=workspace)
+
+
+# ------------------------------------------------------------------------------------ serving
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"
+                     ) -> tuple[torch.Tensor, float]:
+    """(freqs, scale) for rope and paged_append: radians a position of each of the rot / 2 pairs
+    (float64), and what cos and sin are multiplied with.
+
+    scaling, for contexts `factor` times as long as the trained ones: "none"; "linear", positions
+    divided by factor; "ntk", the base raised so that the slowest pair is stretched by factor;
+    "yarn", pairs that turn more than beta_fast times in trained_length kept, those that turn less
+    than beta_slow times stretched by factor, a linear ramp over the pairs between, and cos and sin
+    scaled by 0.1 ln(factor) + 1."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be a positive even number")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    scale = 1.0
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if not beta_fast > beta_slow > 0.0 or trained_length < 1:
+            raise ValueError("yarn wants beta_fast > beta_slow > 0 and a trained length")
+        pair = lambda turns: rot * math.log(trained_length / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+        lo = max(math.floor(pair(beta_fast)), 0)
+        hi = min(math.ceil(pair(beta_slow)), rot - 1)
+        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f * (1 - ramp) + f / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r} (none, linear, ntk, yarn)")
+    return f.to(device), scale
+
+
+def _heads(t: torch.Tensor, name: str, n: int, device, dtype) -> None:
+    if t.dim() != 3 or t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}, heads, dim]")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}")
+    if t.stride(2) != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}: the elements of a head must lie side by side")
+
+
+def _rope_tensor(x: torch.Tensor, y: torch.Tensor | None) -> MsaRopeTensor:
+    sx = x.stride()
+    if y is None:
+        return MsaRopeTensor(x.data_ptr(), None, sx[0], sx[1], 0, 0, x.shape[1], x.shape[2])
+    sy = y.stride()
+    return MsaRopeTensor(x.data_ptr(), y.data_ptr(), sx[0], sx[1], sy[0], sy[1], x.shape[1], x.shape[2])
+
+
+def _no_grad(*tensors) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("the result would carry no gradient: call this under torch.no_grad() "
+                         "(rope(..., backward=True) takes gradients back)")
+
+
+def _small(t: torch.Tensor, name: str, device, dtype, shape) -> int:
+    """Address of a contiguous tensor of known shape, type and device."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _freqs(t: torch.Tensor, name: str, device) -> tuple[int, int]:
+    if t.dtype != torch.float64 or t.dim() != 1 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float64 [rot / 2] on {device}")
+    return t.data_ptr(), 2 * t.shape[0]
+
+
+def _launch(device, fn, *args) -> None:
+    """fn(*args, stream) on the tensors' device, whichever device is the current one."""
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    if st != MSA_OK:
+        _check(st)
+
+
+def rope(x, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False, scale: float = 1.0,
+         backward: bool = False, out=None):
+    """Rotary positions (msa_rope): x [N, heads, dim], or up to four such tensors of the same N
+    tokens (other head counts and dims), bf16, fp16 or fp32; positions [N] int32 or int64; freqs
+    float64 [rot / 2] (rope_frequencies). The first rot elements of every head are rotated, in halves
+    or interleaved pairs, the rest copied. backward=True: the gradient of the result to that of x
+    (same freqs, positions and scale). out: where the results go (x itself: in place)."""
+    lib = load_library()
+    many = isinstance(x, (tuple, list))
+    xs = tuple(x) if many else (x,)
+    if not 1 <= len(xs) <= 4:
+        raise ValueError("rope takes one to four tensors")
+    device, dtype = xs[0].device, xs[0].dtype
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if dtype not in _DTYPES:
+        raise ValueError(f"rope takes bfloat16, float16 and float32, not {dtype}")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError("positions must be int32 or int64")
+    _no_grad(*xs)
+    n = xs[0].shape[0]
+    outs = tuple(torch.empty(t.shape, dtype=dtype, device=device) for t in xs) if out is None else (
+        tuple(out) if many else (out,))
+    if len(outs) != len(xs):
+        raise ValueError("out must match x")
+    arr = (MsaRopeTensor * len(xs))()
+    for i, (a, b) in enumerate(zip(xs, outs)):
+        _heads(a, "x", n, device, dtype)
+        _heads(b, "out", n, device, dtype)
+        if a.shape != b.shape:
+            raise ValueError("out must have x's shape")
+        arr[i] = _rope_tensor(a, b)
+    f, rot = _freqs(freqs, "freqs", device)
+    p = MsaRopeParams(_DTYPES[dtype], rot, int(interleaved), int(backward), scale, int(positions.dtype == torch.int64), f,
+                      _small(positions, "positions", device, positions.dtype, (n,)))
+    _launch(device, lib.msa_rope, p, arr, len(xs), n)
+    return outs if many else outs[0]
+
+
+class PagedCache:
+    """Handle of a paged cache: k_pages, v_pages [pages, page_size, G, d] and k_idx_pages
+    [pages, page_size, G, d_idx], bf16 (see msa_paged_cache in include/msa.h). Pages may lie apart
+    (slices of a larger tensor); a page itself is contiguous. The handle keeps the tensors alive."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_idx_pages: torch.Tensor):
+        load_library()
+        if k_pages.dim() != 4 or k_idx_pages.dim() != 4 or v_pages.shape != k_pages.shape \
+                or k_idx_pages.shape[:3] != k_pages.shape[:3]:
+            raise ValueError("pages must be [pages, page_size, G, dim] of one geometry")
+        self.device = k_pages.device
+        if self.device.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_idx_pages, "k_idx_pages")):
+            if t.dtype != torch.bfloat16 or t.device != self.device:
+                raise ValueError(f"{name} must be bfloat16 on {self.device}")
+            if t.numel() and not t[0].is_contiguous():
+                raise ValueError(f"{name}: a page must be contiguous")
+        self.k_pages, self.v_pages, self.k_idx_pages = k_pages, v_pages, k_idx_pages
+        self.num_pages, self.page_size, self.G, self.d = k_pages.shape
+        self.d_idx = k_idx_pages.shape[3]
+        stride = lambda t: t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t[0].numel())  # noqa: E731
+        self.c = MsaPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), k_idx_pages.data_ptr(), self.num_pages,
+                               stride(k_pages), stride(v_pages), stride(k_idx_pages), self.page_size, self.G, self.d,
+                               self.d_idx)
+
+
+def _table(page_table: torch.Tensor, seqlens: torch.Tensor, device, batch: int) -> None:
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != device \
+            or page_table.shape[0] != batch or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
+        raise ValueError(f"page_table must be int32 [{batch}, pages] on {device}, its rows contiguous")
+    _small(seqlens, "seqlens", device, torch.int32, (batch,))
+
+
+def _table_stride(page_table: torch.Tensor) -> int:
+    return max(page_table.stride(0), page_table.shape[1]) if page_table.shape[0] == 1 else page_table.stride(0)
+
+
+def paged_append(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                 k_idx: torch.Tensor, cu_seqlens: torch.Tensor | None = None, freqs: torch.Tensor | None = None,
+                 idx_freqs: torch.Tensor | None = None, rotate_index: bool = True, interleaved: bool = False,
+                 rope_scale: float = 1.0, q: torch.Tensor | None = None, q_idx: torch.Tensor | None = None,
+                 q_out: torch.Tensor | None = None, q_idx_out: torch.Tensor | None = None
+                 ) -> tuple[torch.Tensor | None, torch.Tensor | None]:
+    """Writes new tokens into the cache (msa_paged_append): k, v [N, G, d], k_idx [N, G, d_idx] in bf16,
+    fp16 or fp32, keys rotated by their positions on the way (freqs given; index keys by idx_freqs, or by
+    freqs, unless rotate_index is False). seqlens [B] int32 counts the new tokens; cu_seqlens [B + 1] int32
+    says which rows are whose (None: N / B each); rows behind cu_seqlens[B] are padding. q [N, Hq, d] and
+    q_idx [N, G, d_idx] are rotated in the same launch into q_out / q_idx_out (bf16; allocated if None,
+    padding rows then undefined). Returns (q_out, q_idx_out)."""
+    lib = load_library()
+    device, dtype, n, batch = cache.device, k.dtype, k.shape[0], seqlens.shape[0]
+    if dtype not in _DTYPES:
+        raise ValueError(f"paged_append takes bfloat16, float16 and float32, not {dtype}")
+    _table(page_table, seqlens, device, batch)
+    _no_grad(k, v, k_idx, q, q_idx)
+    for t, name in ((k, "k"), (v, "v"), (k_idx, "k_idx"), (q, "q"), (q_idx, "q_idx")):
+        if t is not None:
+            _heads(t, name, n, device, dtype)
+    outs = []
+    for t, o, name in ((q, q_out, "q_out"), (q_idx, q_idx_out, "q_idx_out")):
+        if t is None and o is not None:
+            raise ValueError(f"{name} without its input")
+        if t is not None and o is None:
+            o = torch.empty(t.shape, dtype=torch.bfloat16, device=device)
+        elif t is not None:
+            _heads(o, name, n, device, torch.bfloat16)
+            if o.shape != t.shape:
+                raise ValueError(f"{name} must have its input's shape")
+        outs.append(o)
+    f, rot = (None, 0) if freqs is None else _freqs(freqs, "freqs", device)
+    fi, irot = (f, rot) if rotate_index else (None, 0)
+    if idx_freqs is not None:
+        fi, irot = _freqs(idx_freqs, "idx_freqs", device)
+    cu = None if cu_seqlens is None else _small(cu_seqlens, "cu_seqlens", device, torch.int32, (batch + 1,))
+    p = MsaPagedAppendParams(_DTYPES[dtype], batch, page_table.shape[1], int(interleaved), rot, irot, rope_scale,
+                             _table_stride(page_table), page_table.data_ptr(), seqlens.data_ptr(), cu, f, fi)
+    _launch(device, lib.msa_paged_append, cache.c, p, _rope_tensor(k, None), _rope_tensor(v, None),
+            _rope_tensor(k_idx, None), None if q is None else _rope_tensor(q, outs[0]),
+            None if q_idx is None else _rope_tensor(q_idx, outs[1]), n)
+    return outs[0], outs[1]
+
+
+def paged_decode_workspace(cache: PagedCache, batch: int, max_pages: int, hq: int, topk: int, bk: int = 128,
+                           n_new: int = 1) -> int:
+    """Bytes of workspace of paged_decode for page tables of max_pages columns."""
+    p = MsaPagedDecodeParams(hq, batch, n_new, bk, topk, max_pages, 0, 0.0, max_pages, None, None, None)
+    need = load_library().msa_paged_decode_workspace(cache.c, p)
+    if need == 0:
+        raise MsaError(2, load_library().msa_last_error_detail().decode())
+    return need
+
+
+def paged_decode(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Tensor, q: torch.Tensor, q_idx: torch.Tensor,
+                 topk: int, bk: int = 128, scale: float = 0.0, prefix_pages: torch.Tensor | None = None,
+                 block_ids: torch.Tensor | None = None, o: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Decode over a paged cache (msa_paged_decode). q [B, Hq, d] and q_idx [B, G, d_idx] are the newest
+    token's of every sequence, or with a second dimension of 1 to 8 the newest tokens'; their keys are
+    in the cache already (paged_append). page_table [B, pages], seqlens [B] int32. prefix_pages int32
+    [n]: the first n pages of every sequence, where the batch shares a prefix; it is scored once for all.
+    block_ids int32 [..., G, topk] takes the selection. Returns o, shaped as q; rows without a token are 0."""
+    lib = load_library()
+    device, shape = cache.device, q.shape
+    S = 1 if len(shape) == 3 else shape[1]
+    if len(shape) not in (3, 4) or shape[-1] != cache.d:
+        raise ValueError(f"q must be [B, Hq, {cache.d}] or [B, tokens, Hq, {cache.d}]")
+    batch, lead, hq = shape[0], tuple(shape[:-2]), shape[-2]
+    _table(page_table, seqlens, device, batch)
+    _no_grad(q, q_idx)
+    qp = _small(q, "q", device, torch.bfloat16, tuple(shape))
+    qip = _small(q_idx, "q_idx", device, torch.bfloat16, lead + (cache.G, cache.d_idx))
+    idp = None if block_ids is None else _small(block_ids, "block_ids", device, torch.int32, lead + (cache.G, topk))
+    if o is None:
+        o = torch.empty_like(q)
+    op = _small(o, "o", device, torch.bfloat16, tuple(shape))
+    pp, shared = None, 0
+    if prefix_pages is not None:
+        shared = prefix_pages.shape[0]
+        pp = _small(prefix_pages, "prefix_pages", device, torch.int32, (shared,))
+    p = MsaPagedDecodeParams(hq, batch, S, bk, topk, page_table.shape[1], shared, scale, _table_stride(page_table),
+                             page_table.data_ptr(), seqlens.data_ptr(), pp)
+    need = lib.msa_paged_decode_workspace(cache.c, p)
+    if need == 0:
+        raise MsaError(2, lib.msa_last_error_detail().decode())
+    ws = _workspace(need, device, workspace)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    _launch(device, lib.msa_paged_decode, cache.c, p, qp, qip, idp, op, ws.data_ptr(), ws.numel() * ws.element_size())
+    return o
 
 
 def msa_get_device_error(device=None) -> int:

@@ -212,6 +212,116 @@ MSA_API msa_status_t msa_forward_host(const msa_params* p, const void* q, const 
                                       const void* q_idx, const void* k_idx, int32_t* block_ids_out, void* o,
                                       void* device_buf, size_t device_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Serving: rotary positions, a paged cache and decode over it. (No counterpart in the
+ * method's description, which leaves positions and the cache's layout to the model and the
+ * server; the selection and the attention are those of msa_forward's decode.)
+ * ------------------------------------------------------------------------------------ */
+
+typedef enum msa_dtype_t { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP32 = 2 } msa_dtype_t;
+
+/* One tensor of heads, [n, heads, dim]: element e of head h of token t is
+ * x[t * token_stride + h * head_stride + e] (strides in elements; any strides, so a slice of a
+ * fused projection is taken as it lies). y is where the result goes; it may be x itself with
+ * the same strides, and must not overlap it otherwise. dim: even, 2 to 1024; aligned to one
+ * element at least (16-byte aligned pointers and strides take the wide path). */
+typedef struct msa_rope_tensor {
+  const void* x;
+  void* y;
+  int64_t x_token_stride, x_head_stride;
+  int64_t y_token_stride, y_head_stride;
+  int32_t heads, dim;
+} msa_rope_tensor;
+
+/* dtype: msa_dtype_t of the tensors. rot: leading elements of each head that are rotated (even;
+ * the rest is copied). freqs: device double [rot / 2], radians a position of each pair; any
+ * scaling for long contexts is in them. scale multiplies cos and sin (1 without such a scheme).
+ * interleaved: pairs are elements (2f, 2f + 1), else (f, f + rot / 2). backward: the transposed
+ * map, which takes the gradient of the result to the gradient of the input. positions: device
+ * [n], int32 or (positions_i64) int64; any sign. */
+typedef struct msa_rope_params {
+  int32_t dtype, rot, interleaved, backward;
+  float scale;
+  int32_t positions_i64;
+  const double* freqs;
+  const void* positions;
+} msa_rope_params;
+
+/* Rotates up to four tensors of the same tokens in one launch. Computed in fp32 (angles in 64-bit
+ * fixed point) and rounded once. n = 0 does nothing. Needs no workspace; may be captured. */
+MSA_API msa_status_t msa_rope(const msa_rope_params* p, const msa_rope_tensor* tensors, int32_t count, int64_t n,
+                              void* stream);
+
+/* A paged cache: page i of k starts at k + i * k_page_stride elements and holds page_size tokens
+ * of all groups, [page_size, g, d] bf16 (v the same, k_idx with d_idx). page_size: a power of two,
+ * 16 to 1024; strides between pages in elements, multiples of 8, at least a page (so K and V may
+ * alternate in one allocation); d in {64, 128}; d_idx in {32, 64, 128}; g <= 64. Host structure;
+ * the memory is the caller's. */
+typedef struct msa_paged_cache {
+  void *k, *v, *k_idx;
+  int64_t num_pages;
+  int64_t k_page_stride, v_page_stride, k_idx_page_stride;
+  int32_t page_size, g, d, d_idx;
+} msa_paged_cache;
+
+/* The sequences of a call: page_table device int32 [batch, table_stride], of which max_pages
+ * columns count: token t of sequence b lies in page page_table[b][t / page_size]. Entries behind a
+ * sequence's last page are not read. seqlens device int32 [batch]: tokens of each sequence, the
+ * new ones among them. batch <= 4096; max_pages * page_size < 2^26.
+ * cu_seqlens device int32 [batch + 1] (cu_seqlens[0] = 0, not descending): the new tokens of
+ * sequence b are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the tensors; NULL: n / batch each.
+ * freqs / idx_freqs: see msa_rope_params, for q and k / for q_idx and k_idx; NULL: not rotated. */
+typedef struct msa_paged_append_params {
+  int32_t dtype, batch, max_pages, interleaved, rot, idx_rot;
+  float scale;
+  int64_t table_stride;
+  const int32_t* page_table;
+  const int32_t* seqlens;
+  const int32_t* cu_seqlens;
+  const double* freqs;
+  const double* idx_freqs;
+} msa_paged_append_params;
+
+/* Writes the n new tokens' keys, values and index keys into the cache, keys rotated to their
+ * positions on the way, and (q, q_idx not NULL) rotates their queries in the same launch. A
+ * sequence's new tokens are its last ones: row t of sequence b has position
+ * seqlens[b] - (cu_seqlens[b + 1] - t). k, v: g heads of d; k_idx: g heads of d_idx (y ignored: the
+ * pages take the result); q, q_idx: any heads, y bf16. Inputs of type dtype, rounded once to bf16.
+ * Rows from cu_seqlens[batch] on are padding: neither read nor written. A token outside its
+ * sequence's pages, or a page outside the cache, is reported through msa_get_device_error as
+ * MSA_ERR_DEVICE_BOUNDS and left out. Two tokens of a call must not share a slot. Needs no workspace. */
+MSA_API msa_status_t msa_paged_append(const msa_paged_cache* cache, const msa_paged_append_params* p,
+                                      const msa_rope_tensor* k, const msa_rope_tensor* v, const msa_rope_tensor* k_idx,
+                                      const msa_rope_tensor* q, const msa_rope_tensor* q_idx, int64_t n, void* stream);
+
+/* hq: query heads, hq / g <= 16. n_new: 1 to 8 newest tokens of every sequence, whose queries are
+ * given (several: drafted tokens, each seeing those before it). bk, k, scale: as msa_params.
+ * prefix_pages: device int32 [n_prefix_pages]: the first n_prefix_pages pages of EVERY sequence
+ * (a shared prefix; their columns of page_table are then not read, and their index keys are scored
+ * once for the whole batch). n_prefix_pages 0: none. */
+typedef struct msa_paged_decode_params {
+  int32_t hq, batch, n_new, bk, k, max_pages, n_prefix_pages;
+  float scale;
+  int64_t table_stride;
+  const int32_t* page_table;
+  const int32_t* seqlens;
+  const int32_t* prefix_pages;
+} msa_paged_decode_params;
+
+/* Decode over a paged cache: for new token s of sequence b, at position p = seqlens[b] - n_new + s
+ * (already appended), the selection and the attention of msa_forward's decode over the tokens j <= p.
+ * q [batch, n_new, hq, d], q_idx [batch, n_new, g, d_idx] bf16; o [batch, n_new, hq, d] bf16;
+ * block_ids_out int32 [batch, n_new, g, k] or NULL. A row without a token (p < 0: a padded batch,
+ * seqlens[b] = 0) gets zeros and ids of -1. Lengths above the table's and pages outside the cache are
+ * reported as MSA_ERR_DEVICE_BOUNDS; the outputs of such sequences are then undefined (nothing is read
+ * or written out of range). Cache rows behind a sequence's end may hold anything.
+ * Only enqueues launches whose grids depend on the parameters alone: may be captured into a CUDA graph.
+ * Calls that may run at the same time, replays among them, need a workspace each. */
+MSA_API size_t msa_paged_decode_workspace(const msa_paged_cache* cache, const msa_paged_decode_params* p);
+MSA_API msa_status_t msa_paged_decode(const msa_paged_cache* cache, const msa_paged_decode_params* p, const void* q,
+                                      const void* q_idx, int32_t* block_ids_out, void* o, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
 /* Failure reporting of this library (no counterpart in the method's description).
  * Synchronises `stream`, then reads and clears this device's error word. Returns
  * MSA_OK, MSA_ERR_TIMEOUT or MSA_ERR_DEVICE_BOUNDS (the first error recorded since the
