@@ -1506,6 +1506,7 @@ msa_status_t msa_paged_append(const msa_paged_cache* c, const msa_paged_append_p
   P.sign = 1.0f;
   P.n = n;
   P.cu_seqlens = p->cu_seqlens;
+  P.each = p->cu_seqlens ? 0 : int(n / p->batch);
   P.seqlens = p->seqlens;
   P.page_table = p->page_table;
   P.table_stride = p->table_stride;
