@@ -34,6 +34,7 @@ enum KernelId : int {
   kKidPagedScan = 10,
   kKidPagedTopk = 11,
   kKidPagedAttn = 12,
+  kKidPrefixScan = 13,
 };
 
 // Device error word: low byte = first msa_status_t recorded, next byte = kernel id.

@@ -195,6 +195,38 @@ msa_status_t launch_paged_scan(const PagedScanParams& P, cudaStream_t st) {
   return MSA_OK;
 }
 
+template <int DI, int RT>
+msa_status_t launch_prefix_scan(const CUtensorMap& tq, const CUtensorMap& tk, PrefixScanParams P, cudaStream_t st) {
+  using C = PrefixCfg<DI, RT>;
+  static std::once_flag once;
+  static msa_status_t attr = MSA_OK;
+  std::call_once(once, [] { attr = set_smem(prefix_scan_kernel<DI, RT>, C::kSmemBytes); });
+  if (attr != MSA_OK) return fail(attr, "prefix scan: shared memory");
+  const int sms = num_sms();
+  P.pairs = (P.rows + RT * 128 - 1) / (RT * 128) * P.G;
+  P.workers = std::max(1, std::min(sms / P.pairs, P.tiles));
+  const int grid = P.workers > 1 ? P.workers * P.pairs : std::min(sms, P.pairs);
+  ProfScope ps(kPPrefixScan, st);
+  prefix_scan_kernel<DI, RT><<<grid, kPrefixThreads, C::kSmemBytes, st>>>(tq, tk, P);
+  MSA_CHECK_LAUNCH();
+  return MSA_OK;
+}
+
+template <int DI>
+msa_status_t run_prefix_scan(const msa_paged_cache* c, const void* q_idx, const PrefixScanParams& P, cudaStream_t st) {
+  using I = IdxCfg<DI>;
+  const CUtensorMapSwizzle sw = I::kSw64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t row = uint64_t(c->g) * DI * 2;
+  CUtensorMap tq, tk;
+  msa_status_t s;
+  if ((s = make_map_3d(&tq, q_idx, DI, c->g, P.rows, DI * 2, row, I::kPanelElems, 1, 128, sw)) != MSA_OK) return s;
+  if ((s = make_map_4d(&tk, c->k_idx, {uint64_t(DI), uint64_t(c->g), uint64_t(c->page_size), uint64_t(c->num_pages)},
+                       {uint64_t(DI) * 2, row, uint64_t(c->k_idx_page_stride) * 2},
+                       {uint32_t(I::kPanelElems), 1, uint32_t(std::min(c->page_size, 128)), 1}, sw)) != MSA_OK)
+    return s;
+  return P.rows <= 128 ? launch_prefix_scan<DI, 1>(tq, tk, P, st) : launch_prefix_scan<DI, 2>(tq, tk, P, st);
+}
+
 template <int D>
 msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
   using C = PagedAttnCfg<D>;
@@ -237,7 +269,27 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
     sp.bk = p->bk;
     sp.k = p->k;
     sp.nbmax = nbmax;
-    sp.nb0 = 0;
+    // whole blocks of a shared prefix are scored once for all rows
+    if (p->n_prefix_pages > 0) {
+      PrefixScanParams P{};
+      P.prefix = p->prefix_pages;
+      P.maxima = L.maxima;
+      P.num_pages = c->num_pages;
+      P.n_pages = p->n_prefix_pages;
+      P.shift = V.shift;
+      P.rows = p->batch * p->n_new;
+      P.G = c->g;
+      P.bk = p->bk;
+      P.nbmax = nbmax;
+      P.blocks = int(int64_t(p->n_prefix_pages) * c->page_size / p->bk);
+      P.tiles = int((int64_t(P.blocks) * p->bk + 127) / 128);
+      if (P.tiles > 0) {
+        s = c->d_idx == 128 ? run_prefix_scan<128>(c, q_idx, P, st) : c->d_idx == 64 ? run_prefix_scan<64>(c, q_idx, P, st)
+                                                                                     : run_prefix_scan<32>(c, q_idx, P, st);
+        if (s != MSA_OK) return s;
+        sp.nb0 = P.blocks;
+      }
+    }
     s = c->d_idx == 128 ? launch_paged_scan<128>(sp, st) : c->d_idx == 64 ? launch_paged_scan<64>(sp, st) : launch_paged_scan<32>(sp, st);
     if (s != MSA_OK) return s;
   }
