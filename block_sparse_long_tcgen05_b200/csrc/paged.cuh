@@ -179,7 +179,9 @@ struct PagedTopkParams {
   PageView view;
   const uint32_t* maxima;   // [rows][G][nbmax]
   int32_t* block_ids;       // [rows][G][k]
-  int G, bk, k, nbmax;
+  unsigned int* arrived;    // [rows][G]: zeroed here for the attention
+  __nv_bfloat16* o;         // [rows][G][width]: zeroed here where a row has no token
+  int G, bk, k, nbmax, width;
 };
 
 __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__ PagedTopkParams P) {
@@ -192,6 +194,9 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
   int32_t* out = P.block_ids + rg * P.k;
   const int64_t pos = paged_length(V, b, kKidPagedTopk) - V.S + s;
   const int bl = pos >= 0 ? static_cast<int>(pos / P.bk) : -1;
+  if (lane == 0) P.arrived[rg] = 0u;
+  if (bl < 0)
+    for (int e = lane; e < P.width / 8; e += 32) reinterpret_cast<uint4*>(P.o + rg * P.width)[e] = make_uint4(0, 0, 0, 0);
   if (bl + 1 <= P.k) {
     if (lane < P.k) out[lane] = lane <= bl ? lane : -1;
     return;
@@ -235,13 +240,21 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
 
 // ------------------------------------------------------------------------------------
 // Sparse attention of every (row, group) over its selected blocks. Bound by the chosen blocks'
-// bytes. The block's tokens are cut into strips of 16 (a strip lies in one page); every warp
-// takes every fourth strip through its own ring of asynchronous copies, and carries its own
-// running maximum, sum and output, so that warps meet only once, at the end. S = Q K^T and
-// O += P V are m16n8k16 products with the group's R <= 16 heads as rows (too few for tcgen05);
-// a strip's probabilities go from the first product's accumulators straight into the second's
-// operand, rounded to bf16 (off by at most 2^-8 of each weight, what the output is rounded to as well);
-// maximum, sum and output stay in fp32.
+// bytes. The blocks' tokens are cut into strips of 16 (a strip lies in one page). All rows' strips
+// stand in one list, and every CTA of a single resident wave takes an equal run of it, whatever
+// the sequences' lengths; where a run ends inside a (row, group) its result is a part, and the
+// last CTA to finish one of the parts joins them, in the list's order. (One CTA for every
+// (row, group) leaves SMs idle, and clusters that share one wait for each other's places: 32 ragged
+// sequences took 47 and 63 to 87 us, against 48 here; what is left above the
+// bytes' 37 us is the chain of look-ups before the first copy and the join after the last.)
+//
+// A warp takes every fourth strip of the run through its own ring of asynchronous copies and carries
+// its own running maximum, sum and output, so that warps meet only at the end of a (row, group).
+// The products are m16n8k16, transposed so that the group's R <= 16 heads are the columns (too few
+// for tcgen05's rows; one or two tiles of 8): S^T = K Q^T has the strip's tokens as rows, O^T += V^T P^T
+// the output's elements. The probabilities go from the first one's accumulators into the second's
+// operand through a transposition in registers (movmatrix), rounded to bf16 (off by at most 2^-8 of
+// each weight, what the output is rounded to as well); maximum, sum and output stay in fp32.
 // ------------------------------------------------------------------------------------
 struct PagedAttnParams {
   PageView view;
@@ -251,19 +264,25 @@ struct PagedAttnParams {
   int64_t k_stride, v_stride;
   const int32_t* block_ids;    // [rows][G][k]
   __nv_bfloat16* o;            // [batch][S][G * R][D]
+  float* parts;                // [2 * CTAs][R][D + 2]: O, then m and l; part 2 c continues a unit, 2 c + 1 begins one
+  unsigned int* arrived;       // [rows][G] parts written so far (zeroed by the Top-k)
   int G, R, k, bk;
   float scale_log2;
 };
 
 constexpr int kPagedAttnWarps = 4;
-constexpr int kPagedAttnRing = 3;
+constexpr int kPagedAttnTable = 512;   // strips looked up at a time
+constexpr int kPagedAttnRing = 2;
+constexpr int kPagedAttnLeast = 16;    // strips of a run, where there are enough: shorter ones cost more to join than they save
 template <int D>
 struct PagedAttnCfg {
-  static constexpr int kPitch = D + 8;                       // padded: ldmatrix rows hit distinct banks
-  static constexpr int kStrip = 2 * 16 * kPitch;             // elements of a strip's K and V
-  static constexpr int kRingBytes = kPagedAttnWarps * kPagedAttnRing * kStrip * 2;
-  static constexpr int kOutBytes = kPagedAttnWarps * (16 * D + 32) * 4;   // O, m, l of every warp (over the ring)
-  static constexpr int kSmemBytes = kRingBytes > kOutBytes ? kRingBytes : kOutBytes;
+  static constexpr int kStrip = 2 * 16 * D;                  // elements of a strip's K and V
+  static constexpr int kPitch = D + 4;                       // of a head's O: the lanes' stores hit distinct banks
+  static constexpr int kEight = 8 * kPitch + 16;             // floats of 8 heads' O, m and l
+  static constexpr int kJoinOff = kPagedAttnWarps * kPagedAttnRing * kStrip * 2;
+  static constexpr int kTableOff = kJoinOff + 2 * kEight * 4;
+  static constexpr int kEndsOff = kTableOff + kPagedAttnTable * 8;
+  static constexpr int smem_bytes(int batch) { return kEndsOff + batch * 4; }
 };
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], const void* row_addr) {
@@ -279,192 +298,323 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], const void* row_
                : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPagedAttnWarps * 32) paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
+// Transposes an 8 x 8 matrix of 16-bit elements held as a fragment (row lane / 4, columns 2 (lane % 4) ..).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// A place in the list of strips: strip `at` of the `n` strips of (sequence b, new token s, group g);
+// `unit` is the first of them in the list.
+struct StripPlace {
+  int b, s, g, n, at;
+  int64_t pos, unit;
+};
+
+// Strips of one group of new token s of a sequence of length L.
+__device__ __forceinline__ int row_strips(int64_t L, int S, int s, int k, int bk) {
+  const int64_t pos = L - S + s;
+  return pos < 0 ? 0 : min(k, static_cast<int>(pos / bk) + 1) * (bk >> 4);
+}
+
+// ends[b]: strips of sequences 0 .. b, divided by G.
+__device__ __forceinline__ StripPlace find_strip(const PagedAttnParams& P, const int* ends, int64_t t) {
+  const PageView& V = P.view;
+  const int tg = static_cast<int>(t / P.G);   // a sequence's strips are a multiple of G
+  int lo = 0, hi = V.batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > tg) hi = mid; else lo = mid + 1;
+  }
+  StripPlace x;
+  x.b = lo;
+  const int64_t L = V.seqlens[lo];
+  x.unit = lo > 0 ? static_cast<int64_t>(ends[lo - 1]) * P.G : 0;
+  for (x.s = 0;; ++x.s) {
+    x.n = row_strips(L, V.S, x.s, P.k, P.bk);
+    if (t < x.unit + static_cast<int64_t>(x.n) * P.G || x.s + 1 == V.S) break;
+    x.unit += static_cast<int64_t>(x.n) * P.G;
+  }
+  x.g = static_cast<int>((t - x.unit) / x.n);
+  x.unit += static_cast<int64_t>(x.g) * x.n;
+  x.at = static_cast<int>(t - x.unit);
+  x.pos = L - V.S + x.s;
+  return x;
+}
+
+// NT: tiles of 8 heads.
+template <int D, int NT>
+__global__ void __launch_bounds__(kPagedAttnWarps * 32, 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
   using C = PagedAttnCfg<D>;
+  constexpr int kThreads = kPagedAttnWarps * 32;
   extern __shared__ __align__(16) uint8_t psm[];
+  __shared__ int warp_sum[kPagedAttnWarps];
+  __shared__ int is_last;
   const PageView& V = P.view;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
-  const int64_t rg = blockIdx.x;
-  const int64_t row = rg / P.G;
-  const int g = static_cast<int>(rg - row * P.G);
-  const int b = static_cast<int>(row / V.S), s = static_cast<int>(row % V.S);
-  const int64_t pos = paged_length(V, b, kKidPagedAttn) - V.S + s;
-  const int32_t* ids = P.block_ids + rg * P.k;
-  const int64_t head0 = (row * P.G + g) * P.R;
-
-  // the warp's strips: strip i of the row is strip i % per_block of slot i / per_block
-  const int per_block = P.bk >> 4;
-  int slots = 0;
-  if (pos >= 0) {
-    const int bl = static_cast<int>(pos / P.bk);
-    slots = min(P.k, bl + 1);
-  }
-  const int strips = slots * per_block;
-
-  uint32_t qf[D / 16][4];
-  {
-    const __nv_bfloat16* q0 = P.q + head0 * D;
-    auto pair = [&](int r, int col) -> uint32_t {
-      return r < P.R ? *reinterpret_cast<const uint32_t*>(q0 + r * D + col) : 0u;
-    };
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      qf[kk][0] = pair(gq, kk * 16 + 2 * tq);
-      qf[kk][1] = pair(gq + 8, kk * 16 + 2 * tq);
-      qf[kk][2] = pair(gq, kk * 16 + 8 + 2 * tq);
-      qf[kk][3] = pair(gq + 8, kk * 16 + 8 + 2 * tq);
+  float* join = reinterpret_cast<float*>(psm + C::kJoinOff);
+  int2* table = reinterpret_cast<int2*>(psm + C::kTableOff);   // page; row in the page, group, tokens seen
+  int* ends = reinterpret_cast<int*>(psm + C::kEndsOff);
+  // running total of the sequences' strips
+  int total = 0;
+  for (int b0 = 0; b0 < V.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int x = 0;
+    if (b < V.batch) {
+      const int64_t L = paged_length(V, b, kKidPagedAttn);
+      for (int s = 0; L > 0 && s < V.S; ++s) x += row_strips(L, V.S, s, P.k, P.bk);
     }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = total;
+    for (int w = 0; w < kPagedAttnWarps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    if (b < V.batch) ends[b] = before + x;
+    __syncthreads();
   }
+  const int64_t strips = static_cast<int64_t>(total) * P.G;
+  const int64_t run = max(static_cast<int64_t>(kPagedAttnLeast), (strips + gridDim.x - 1) / gridDim.x);
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * run;
+  const int64_t end = min(strips, begin + run);
+
   __nv_bfloat16* ring = reinterpret_cast<__nv_bfloat16*>(psm) + warp * kPagedAttnRing * C::kStrip;
-  // starts the copies of strip i and returns how many of its tokens the row sees
-  auto fetch = [&](int i, int stage) -> int {
-    int seen = 0;
-    if (i < strips) {
-      const int blk = __ldg(ids + i / per_block);
-      const int64_t t0 = static_cast<int64_t>(blk) * P.bk + (i % per_block) * 16;
-      const bool in_order = blk >= 0 && t0 <= pos;   // else: behind the row's position, or no block
-      int64_t page = -1;
-      if (in_order) page = page_of(V, b, t0, kKidPagedAttn);
-      seen = page >= 0 ? static_cast<int>(min(static_cast<int64_t>(16), pos - t0 + 1)) : 0;
+  const int64_t row = static_cast<int64_t>(P.G) * D;
+  // starts the copies of entry i of the table
+  auto fetch = [&](int i, int count, int stage) {
+    if (i < count) {
+      const int2 at = table[i];
+      const int seen = at.y & 31;
       if (seen > 0) {
-        const int64_t off = (t0 & ((1 << V.shift) - 1)) * P.G * D + g * D;
-        const __nv_bfloat16* ks = P.kp + page * P.k_stride + off;
-        const __nv_bfloat16* vs = P.vp + page * P.v_stride + off;
+        const int64_t off = static_cast<int64_t>(at.y >> 16) * row + ((at.y >> 8) & 255) * D;
+        const __nv_bfloat16* ks = P.kp + at.x * P.k_stride + off;
+        const __nv_bfloat16* vs = P.vp + at.x * P.v_stride + off;
         __nv_bfloat16* kd = ring + stage * C::kStrip;
-        __nv_bfloat16* vd = kd + 16 * C::kPitch;
+        __nv_bfloat16* vd = kd + 16 * D;
 #pragma unroll
         for (int e = lane; e < 16 * (D / 8); e += 32) {
-          const int r = e / (D / 8), c = (e % (D / 8)) * 8;
+          const int r = e / (D / 8), c = e % (D / 8);
           const bool ok = r < seen;   // rows behind the position read as zeros, whatever lies there
-          const int64_t so = ok ? static_cast<int64_t>(r) * P.G * D + c : 0;
-          cp_async16(kd + r * C::kPitch + c, ks + so, ok);
-          cp_async16(vd + r * C::kPitch + c, vs + so, ok);
+          const int64_t so = ok ? r * row + c * 8 : 0;
+          const int to = r * D + ((c ^ (r & 7)) * 8);   // swizzled: ldmatrix rows hit distinct banks
+          cp_async16(kd + to, ks + so, ok);
+          cp_async16(vd + to, vs + so, ok);
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    return seen;
   };
 
-  float o[D / 8][4];
+  uint32_t qf[NT][D / 16][2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];   // heads 8 t + 2 tq and the next
+  bool begun = false;   // the unit's registers hold strips of an earlier table
+  for (int64_t sub = begin; sub < end; sub += kPagedAttnTable) {
+    const int count = static_cast<int>(min(static_cast<int64_t>(kPagedAttnTable), end - sub));
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+      const StripPlace x = find_strip(P, ends, sub + i);
+      const int per_block = P.bk >> 4;
+      const int blk = __ldg(P.block_ids + ((static_cast<int64_t>(x.b) * V.S + x.s) * P.G + x.g) * P.k + x.at / per_block);
+      const int64_t t0 = static_cast<int64_t>(blk) * P.bk + (x.at % per_block) * 16;
+      int64_t page = -1;
+      if (blk >= 0 && t0 <= x.pos) page = page_of(V, x.b, t0, kKidPagedAttn);
+      const int seen = page >= 0 ? static_cast<int>(min(static_cast<int64_t>(16), x.pos - t0 + 1)) : 0;
+      table[i] = make_int2(static_cast<int>(page),
+                           (static_cast<int>(t0) & ((1 << V.shift) - 1)) << 16 | x.g << 8 | seen);
+    }
+    __syncthreads();
+    int i = warp, stage = 0;
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n)
+    for (int st = 0; st < kPagedAttnRing - 1; ++st) fetch(warp + st * kPagedAttnWarps, count, st);
+    for (int cur = 0; cur < count;) {
+      const StripPlace x = find_strip(P, ends, sub + cur);
+      const int stop = static_cast<int>(min(static_cast<int64_t>(count), x.unit + x.n - sub));
+      const int64_t rg = (static_cast<int64_t>(x.b) * V.S + x.s) * P.G + x.g;
+      const int64_t head0 = rg * P.R;
+      if (!begun) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) o[n][x] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // rows gq and gq + 8
-  int seen[kPagedAttnRing];
+        for (int t = 0; t < NT; ++t) {
+          const int r = t * 8 + gq;
+          const uint32_t* q0 = reinterpret_cast<const uint32_t*>(P.q + (head0 + r) * D);
 #pragma unroll
-  for (int st = 0; st < kPagedAttnRing - 1; ++st) seen[st] = fetch(warp + st * kPagedAttnWarps, st);
-  int i = warp;
-  while (i < strips) {
+          for (int kk = 0; kk < D / 16; ++kk) {
+            qf[t][kk][0] = r < P.R ? __ldg(q0 + kk * 8 + tq) : 0u;
+            qf[t][kk][1] = r < P.R ? __ldg(q0 + kk * 8 + 4 + tq) : 0u;
 #pragma unroll
-    for (int st = 0; st < kPagedAttnRing; ++st) {   // unrolled over the ring: stage numbers are constants
-      if (i >= strips) break;
-      __syncwarp();   // every lane is done with the stage that is refilled now
-      seen[(st + kPagedAttnRing - 1) % kPagedAttnRing] =
-          fetch(i + (kPagedAttnRing - 1) * kPagedAttnWarps, (st + kPagedAttnRing - 1) % kPagedAttnRing);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kPagedAttnRing - 1) : "memory");
-      __syncwarp();
-      const int nv = seen[st];
-      if (nv > 0) {
-        const __nv_bfloat16* ks = ring + st * C::kStrip;
-        const __nv_bfloat16* vs = ks + 16 * C::kPitch;
-        float sc[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[n][x] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t bf[4];
-          ldsm_x4(bf, ks + ((lane & 7) + ((lane >> 4) << 3)) * C::kPitch + kk * 16 + ((lane >> 3) & 1) * 8);
-          mma_16816(sc[0], qf[kk], {bf[0], bf[1]});
-          mma_16816(sc[1], qf[kk], {bf[2], bf[3]});
-        }
-        float top[2] = {m[0], m[1]};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int t = n * 8 + 2 * tq + (x & 1);
-            sc[n][x] = t < nv ? sc[n][x] * P.scale_log2 : -INFINITY;
-            top[x >> 1] = fmaxf(top[x >> 1], sc[n][x]);
+            for (int y = 0; y < 4; ++y) o[t][kk][y] = 0.0f;
           }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-          const float from = top[h] == -INFINITY ? 0.0f : top[h];   // every score so far is -inf
-          const float keep = exp2f(m[h] - from);
-          m[h] = top[h];
-          top[h] = from;
-          l[h] *= keep;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            o[n][2 * h] *= keep;
-            o[n][2 * h + 1] *= keep;
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            sc[n][x] = exp2f(sc[n][x] - top[x >> 1]);
-            l[x >> 1] += sc[n][x];
-          }
-        const uint32_t pf[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
-                                pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t bf[4];
-          ldsm_x4_trans(bf, vs + (lane & 15) * C::kPitch + n * 16 + (lane >> 4) * 8);
-          mma_16816(o[2 * n], pf, {bf[0], bf[1]});
-          mma_16816(o[2 * n + 1], pf, {bf[2], bf[3]});
+          m[t][0] = m[t][1] = -INFINITY;
+          l[t][0] = l[t][1] = 0.0f;
         }
       }
-      i += kPagedAttnWarps;
+      for (; i < stop; i += kPagedAttnWarps) {
+        __syncwarp();   // every lane is done with the stage that is refilled now
+        fetch(i + (kPagedAttnRing - 1) * kPagedAttnWarps, count, stage == 0 ? kPagedAttnRing - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kPagedAttnRing - 1) : "memory");
+        __syncwarp();
+        const int nv = table[i].y & 31;
+        const __nv_bfloat16* ks = ring + stage * C::kStrip;
+        const __nv_bfloat16* vs = ks + 16 * D;
+        stage = stage + 1 == kPagedAttnRing ? 0 : stage + 1;
+        if (nv == 0) continue;
+        // S^T: even and odd steps apart, two shorter chains
+        float sc[NT][2][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) sc[t][0][y] = sc[t][1][y] = 0.0f;
+        const int kr = lane & 15;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t af[4];
+          ldsm_x4(af, ks + kr * D + (((kk * 2 + (lane >> 4)) ^ (kr & 7)) * 8));
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_16816(sc[t][kk & 1], af, qf[t][kk]);
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float x[4], top[2] = {m[t][0], m[t][1]};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            x[y] = gq + 8 * (y >> 1) < nv ? (sc[t][0][y] + sc[t][1][y]) * P.scale_log2 : -INFINITY;
+            top[y & 1] = fmaxf(top[y & 1], x[y]);
+          }
+          float keep[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], off));
+            const float from = top[h] == -INFINITY ? 0.0f : top[h];   // every score so far is -inf
+            keep[h] = exp2f(m[t][h] - from);
+            m[t][h] = top[h];
+            top[h] = from;
+            l[t][h] *= keep[h];
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            x[y] = exp2f(x[y] - top[y & 1]);
+            l[t][y & 1] += x[y];
+          }
+          pf[t][0] = transpose_8x8(pack_bf16x2(x[0], x[1]));
+          pf[t][1] = transpose_8x8(pack_bf16x2(x[2], x[3]));
+          if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) o[t][n][y] *= keep[y & 1];
+          }
+        }
+        const int vr = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t af[4];
+          ldsm_x4_trans(af, vs + vr * D + (((n * 2 + ((lane >> 3) & 1)) ^ (vr & 7)) * 8));
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_16816(o[t][n], af, pf[t]);
+        }
+      }
+      cur = stop;
+      begun = sub + cur < x.unit + x.n && sub + cur < end;   // the next table goes on with this unit
+      if (begun) continue;
+
+      // the warps' results, eight heads at a time: warps 2 and 3 into 0 and 1, 1 into 0, that out
+      const int64_t first_cta = x.unit / run, last_cta = (x.unit + x.n - 1) / run;
+      const bool whole = first_cta == last_cta;
+      float* part = P.parts + (2 * static_cast<int64_t>(blockIdx.x) + (first_cta == blockIdx.x ? 1 : 0)) * P.R * (D + 2);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], off);
+        auto put = [&](float* area) {
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) area[(2 * tq + (y & 1)) * C::kPitch + n * 16 + gq + 8 * (y >> 1)] = o[t][n][y];
+          if (gq < 2) *reinterpret_cast<float2*>(area + 8 * C::kPitch + 2 * (2 * tq + gq)) = make_float2(m[t][gq], l[t][gq]);
+        };
+#pragma unroll
+        for (int step = 2; step > 0; step >>= 1) {
+          float* area = join + (step == 2 ? warp & 1 : 0) * C::kEight;
+          if (warp >= step && warp < 2 * step) put(area);
+          __syncthreads();
+          if (warp < step) {
+            float mine[2], theirs[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float2 ml = *reinterpret_cast<const float2*>(area + 8 * C::kPitch + 2 * (2 * tq + h));
+              const float top = fmaxf(m[t][h], ml.x);
+              mine[h] = m[t][h] == -INFINITY ? 0.0f : exp2f(m[t][h] - top);   // 0: a warp without a token
+              theirs[h] = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+              m[t][h] = top;
+              l[t][h] = l[t][h] * mine[h] + ml.y * theirs[h];
+            }
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                o[t][n][y] = o[t][n][y] * mine[y & 1] +
+                             area[(2 * tq + (y & 1)) * C::kPitch + n * 16 + gq + 8 * (y >> 1)] * theirs[y & 1];
+          }
+          __syncthreads();
+        }
+        if (warp == 0) put(join);
+        __syncthreads();
+        for (int e = threadIdx.x; e < 8 * (D / 2); e += kThreads) {
+          const int r8 = e / (D / 2), c = (e % (D / 2)) * 2, r = t * 8 + r8;
+          if (r >= P.R) break;
+          const float2 v = *reinterpret_cast<const float2*>(join + r8 * C::kPitch + c);
+          const float2 ml = *reinterpret_cast<const float2*>(join + 8 * C::kPitch + 2 * r8);
+          if (whole) {
+            const float inv = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;   // nothing but bad pages: zero
+            *reinterpret_cast<uint32_t*>(P.o + (head0 + r) * D + c) = pack_bf16x2(v.x * inv, v.y * inv);
+          } else {
+            *reinterpret_cast<float2*>(part + r * D + c) = v;
+            if (c == 0) *reinterpret_cast<float2*>(part + P.R * D + 2 * r) = ml;
+          }
+        }
+        __syncthreads();   // the area is written again
+      }
+      if (whole) continue;
+      // the last of the unit's CTAs to get here joins the parts
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) is_last = atomicAdd(P.arrived + rg, 1u) == static_cast<unsigned int>(last_cta - first_cta);
+      __syncthreads();
+      if (is_last) {
+        __threadfence();
+        for (int e = threadIdx.x; e < P.R * (D / 2); e += kThreads) {
+          const int r = e / (D / 2), c = (e % (D / 2)) * 2;
+          float top = -INFINITY, sum = 0.0f, u = 0.0f, v = 0.0f;
+          for (int64_t w = first_cta; w <= last_cta; ++w) {
+            const float* from = P.parts + (2 * w + (w == first_cta ? 1 : 0)) * P.R * (D + 2);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + P.R * D + 2 * r));
+            const float2 ov = __ldcg(reinterpret_cast<const float2*>(from + r * D + c));
+            const float higher = fmaxf(top, ml.x);
+            const float a = top == -INFINITY ? 0.0f : exp2f(top - higher), f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - higher);
+            top = higher;
+            sum = sum * a + ml.y * f;
+            u = u * a + ov.x * f;
+            v = v * a + ov.y * f;
+          }
+          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          *reinterpret_cast<uint32_t*>(P.o + (head0 + r) * D + c) = pack_bf16x2(u * inv, v * inv);
+        }
+      }
+      __syncthreads();   // is_last is written again by the next unit
     }
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-  }
-  __syncthreads();   // the ring's memory now takes every warp's O, m and l
-  float* mine = reinterpret_cast<float*>(psm) + warp * (16 * D + 32);
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n) {
-    *reinterpret_cast<float2*>(mine + gq * D + n * 8 + 2 * tq) = make_float2(o[n][0], o[n][1]);
-    *reinterpret_cast<float2*>(mine + (gq + 8) * D + n * 8 + 2 * tq) = make_float2(o[n][2], o[n][3]);
-  }
-  if (tq == 0) {
-    mine[16 * D + gq] = m[0];
-    mine[16 * D + gq + 8] = m[1];
-    mine[16 * D + 16 + gq] = l[0];
-    mine[16 * D + 24 + gq] = l[1];
-  }
-  __syncthreads();
-  const float* all = reinterpret_cast<const float*>(psm);
-  for (int e = threadIdx.x; e < P.R * D / 2; e += blockDim.x) {
-    const int r = e / (D / 2), c = (e % (D / 2)) * 2;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kPagedAttnWarps; ++w) top = fmaxf(top, all[w * (16 * D + 32) + 16 * D + r]);
-    float sum = 0.0f, x = 0.0f, y = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kPagedAttnWarps; ++w) {
-      const float* from = all + w * (16 * D + 32);
-      const float mw = from[16 * D + r];
-      const float f = mw == -INFINITY ? 0.0f : exp2f(mw - top);   // a warp without a token
-      sum += f * from[16 * D + 16 + r];
-      x += f * from[r * D + c];
-      y += f * from[r * D + c + 1];
-    }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;   // a row without a token: zero
-    *reinterpret_cast<uint32_t*>(P.o + (head0 + r) * D + c) = pack_bf16x2(x * inv, y * inv);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();   // the table is written again
   }
 }
 

@@ -140,9 +140,14 @@ msa_status_t check_sequences(const msa_paged_cache* c, int32_t batch, int32_t ma
   return MSA_OK;
 }
 
+// CTAs of the paged attention: two an SM are resident at once.
+int paged_attn_ctas() { return 2 * num_sms(); }
+
 struct PagedLayout {
   uint32_t* maxima = nullptr;
   int32_t* block_ids = nullptr;
+  float* parts = nullptr;
+  unsigned int* arrived = nullptr;
   size_t bytes = 0;
 };
 
@@ -156,6 +161,8 @@ PagedLayout paged_layout(void* ws, const msa_paged_cache* c, const msa_paged_dec
   PagedLayout L;
   L.maxima = static_cast<uint32_t*>(cv.take(size_t(rows) * c->g * paged_blocks(c, p) * 4));
   L.block_ids = static_cast<int32_t*>(cv.take(size_t(rows) * c->g * p->k * 4));   // used when the caller takes none
+  L.parts = static_cast<float*>(cv.take(size_t(2) * paged_attn_ctas() * (p->hq / c->g) * (c->d + 2) * 4));
+  L.arrived = static_cast<unsigned int*>(cv.take(size_t(rows) * c->g * 4));
   L.bytes = cv.off;
   return L;
 }
@@ -227,16 +234,17 @@ msa_status_t run_prefix_scan(const msa_paged_cache* c, const void* q_idx, const 
   return P.rows <= 128 ? launch_prefix_scan<DI, 1>(tq, tk, P, st) : launch_prefix_scan<DI, 2>(tq, tk, P, st);
 }
 
-template <int D>
+template <int D, int NT>
 msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
   using C = PagedAttnCfg<D>;
   static std::once_flag once;
   static msa_status_t attr = MSA_OK;
-  std::call_once(once, [] { attr = set_smem(paged_attn_kernel<D>, C::kSmemBytes); });
+  std::call_once(once, [] { attr = set_smem(paged_attn_kernel<D, NT>, C::smem_bytes(kScanMaxBatch)); });
   if (attr != MSA_OK) return fail(attr, "paged attention: shared memory");
-  const int64_t grid = int64_t(P.view.batch) * P.view.S * P.G;
+  const int64_t most = int64_t(P.view.batch) * P.view.S * P.G * P.k * (P.bk / 16);   // strips
+  const int64_t grid = std::min<int64_t>(paged_attn_ctas(), (most + kPagedAttnLeast - 1) / kPagedAttnLeast);
   ProfScope ps(kPPagedAttn, st);
-  paged_attn_kernel<D><<<unsigned(grid), kPagedAttnWarps * 32, C::kSmemBytes, st>>>(P);
+  paged_attn_kernel<D, NT><<<unsigned(grid), kPagedAttnWarps * 32, C::smem_bytes(P.view.batch), st>>>(P);
   MSA_CHECK_LAUNCH();
   return MSA_OK;
 }
@@ -301,6 +309,9 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
   tp.bk = p->bk;
   tp.k = p->k;
   tp.nbmax = nbmax;
+  tp.arrived = L.arrived;
+  tp.o = static_cast<__nv_bfloat16*>(o);
+  tp.width = p->hq / c->g * c->d;
   const int64_t rg = int64_t(p->batch) * p->n_new * c->g;
   {
     ProfScope ps(kPPagedTopk, st);
@@ -316,10 +327,13 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
   ap.v_stride = c->v_page_stride;
   ap.block_ids = ids;
   ap.o = static_cast<__nv_bfloat16*>(o);
+  ap.parts = L.parts;
+  ap.arrived = L.arrived;
   ap.G = c->g;
   ap.R = p->hq / c->g;
   ap.k = p->k;
   ap.bk = p->bk;
   ap.scale_log2 = (p->scale == 0.0f ? 1.0f / std::sqrt(float(c->d)) : p->scale) * 1.4426950408889634f;
-  return c->d == 128 ? launch_paged_attn<128>(ap, st) : launch_paged_attn<64>(ap, st);
+  if (ap.R <= 8) return c->d == 128 ? launch_paged_attn<128, 1>(ap, st) : launch_paged_attn<64, 1>(ap, st);
+  return c->d == 128 ? launch_paged_attn<128, 2>(ap, st) : launch_paged_attn<64, 2>(ap, st);
 }
