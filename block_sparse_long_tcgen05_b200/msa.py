@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -359,49 +360,74 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
     return f.to(device), scale
 
 
-def _heads(t: torch.Tensor, name: str, n: int, device, dtype) -> None:
-    if t.dim() != 3 or t.shape[0] != n:
+# The serving calls are made once a layer and step, on tensors that a GPU is done with in a few
+# microseconds: their parameter structures are packed directly (the layouts of the ctypes
+# structures above), and each tensor is looked at once.
+_PACK_TENSOR = struct.Struct("@PPqqqqii").pack
+_PACK_ROPE = struct.Struct("@iiiifiPP").pack
+_PACK_APPEND = struct.Struct("@iiiiiifqPPPPP").pack
+_PACK_DECODE = struct.Struct("@iiiiiiifqPPP").pack
+_fast = None
+
+
+def _serving():
+    """The serving entry points, taking packed structures."""
+    global _fast
+    if _fast is None:
+        lib = load_library()
+        c_i32, c_i64, c_sz, c_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+        out = []
+        for name, res, args in (("msa_rope", c_i32, [c_p, c_p, c_i32, c_i64, c_p]),
+                                ("msa_paged_append", c_i32, [c_p] * 7 + [c_i64, c_p]),
+                                ("msa_paged_decode_workspace", c_sz, [c_p, c_p]),
+                                ("msa_paged_decode", c_i32, [c_p] * 7 + [c_sz, c_p])):
+            fn = lib[name]
+            fn.restype, fn.argtypes = res, args
+            out.append(fn)
+        _fast = out
+    return _fast
+
+
+def _heads(x: torch.Tensor, name: str, n: int, index: int, dtype, y: torch.Tensor | None = None, y_dtype=None) -> bytes:
+    """Checks a tensor of heads (and the one its result goes to) and packs its msa_rope_tensor."""
+    shape, sx = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != n:
         raise ValueError(f"{name} must be [{n}, heads, dim]")
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} on {device}")
-    if t.stride(2) != 1 and t.shape[2] != 1:
+    if x.dtype != dtype or x.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} on device {index}")
+    if sx[2] != 1 and shape[2] != 1:
         raise ValueError(f"{name}: the elements of a head must lie side by side")
-
-
-def _rope_tensor(x: torch.Tensor, y: torch.Tensor | None) -> MsaRopeTensor:
-    sx = x.stride()
-    if y is None:
-        return MsaRopeTensor(x.data_ptr(), None, sx[0], sx[1], 0, 0, x.shape[1], x.shape[2])
-    sy = y.stride()
-    return MsaRopeTensor(x.data_ptr(), y.data_ptr(), sx[0], sx[1], sy[0], sy[1], x.shape[1], x.shape[2])
-
-
-def _no_grad(*tensors) -> None:
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("the result would carry no gradient: call this under torch.no_grad() "
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: the result would carry no gradient; call this under torch.no_grad() "
                          "(rope(..., backward=True) takes gradients back)")
+    if y is None:
+        return _PACK_TENSOR(x.data_ptr(), 0, sx[0], sx[1], 0, 0, shape[1], shape[2])
+    sy = y.stride()
+    if y.shape != shape or y.dtype != y_dtype or y.get_device() != index or (sy[2] != 1 and shape[2] != 1):
+        raise ValueError(f"{name}: its result must be {y_dtype} {list(shape)} on device {index}, heads' elements side by side")
+    return _PACK_TENSOR(x.data_ptr(), y.data_ptr(), sx[0], sx[1], sy[0], sy[1], shape[1], shape[2])
 
 
-def _small(t: torch.Tensor, name: str, device, dtype, shape) -> int:
+def _small(t: torch.Tensor, name: str, index: int, dtype, shape) -> int:
     """Address of a contiguous tensor of known shape, type and device."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} on {device}")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} on device {index}")
     return t.data_ptr()
 
 
-def _freqs(t: torch.Tensor, name: str, device) -> tuple[int, int]:
-    if t.dtype != torch.float64 or t.dim() != 1 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float64 [rot / 2] on {device}")
+def _freqs(t: torch.Tensor, name: str, index: int) -> tuple[int, int]:
+    if t.dtype != torch.float64 or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float64 [rot / 2] on device {index}")
     return t.data_ptr(), 2 * t.shape[0]
 
 
-def _launch(device, fn, *args) -> None:
+def _launch(index: int, fn, *args) -> None:
     """fn(*args, stream) on the tensors' device, whichever device is the current one."""
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(device))
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(device))
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != MSA_OK:
         _check(st)
 
@@ -413,35 +439,28 @@ def rope(x, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = Fa
     float64 [rot / 2] (rope_frequencies). The first rot elements of every head are rotated, in halves
     or interleaved pairs, the rest copied. backward=True: the gradient of the result to that of x
     (same freqs, positions and scale). out: where the results go (x itself: in place)."""
-    lib = load_library()
     many = isinstance(x, (tuple, list))
     xs = tuple(x) if many else (x,)
     if not 1 <= len(xs) <= 4:
         raise ValueError("rope takes one to four tensors")
-    device, dtype = xs[0].device, xs[0].dtype
-    if device.type != "cuda":
+    dtype, index, n = xs[0].dtype, xs[0].get_device(), xs[0].shape[0]
+    if index < 0:
         raise ValueError("expected CUDA tensors")
     if dtype not in _DTYPES:
         raise ValueError(f"rope takes bfloat16, float16 and float32, not {dtype}")
-    if positions.dtype not in (torch.int32, torch.int64):
+    if positions.dtype != torch.int64 and positions.dtype != torch.int32:
         raise ValueError("positions must be int32 or int64")
-    _no_grad(*xs)
-    n = xs[0].shape[0]
-    outs = tuple(torch.empty(t.shape, dtype=dtype, device=device) for t in xs) if out is None else (
-        tuple(out) if many else (out,))
-    if len(outs) != len(xs):
-        raise ValueError("out must match x")
-    arr = (MsaRopeTensor * len(xs))()
-    for i, (a, b) in enumerate(zip(xs, outs)):
-        _heads(a, "x", n, device, dtype)
-        _heads(b, "out", n, device, dtype)
-        if a.shape != b.shape:
-            raise ValueError("out must have x's shape")
-        arr[i] = _rope_tensor(a, b)
-    f, rot = _freqs(freqs, "freqs", device)
-    p = MsaRopeParams(_DTYPES[dtype], rot, int(interleaved), int(backward), scale, int(positions.dtype == torch.int64), f,
-                      _small(positions, "positions", device, positions.dtype, (n,)))
-    _launch(device, lib.msa_rope, p, arr, len(xs), n)
+    if out is None:
+        outs = tuple(torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs)
+    else:
+        outs = tuple(out) if many else (out,)
+        if len(outs) != len(xs):
+            raise ValueError("out must match x")
+    f, rot = _freqs(freqs, "freqs", index)
+    p = _PACK_ROPE(_DTYPES[dtype], rot, bool(interleaved), bool(backward), scale, positions.dtype == torch.int64, f,
+                   _small(positions, "positions", index, positions.dtype, (n,)))
+    tensors = b"".join([_heads(a, "x", n, index, dtype, b, dtype) for a, b in zip(xs, outs)])
+    _launch(index, _serving()[0], p, tensors, len(xs), n)
     return outs if many else outs[0]
 
 
@@ -467,20 +486,21 @@ class PagedCache:
         self.num_pages, self.page_size, self.G, self.d = k_pages.shape
         self.d_idx = k_idx_pages.shape[3]
         stride = lambda t: t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t[0].numel())  # noqa: E731
+        self.index = self.device.index
         self.c = MsaPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), k_idx_pages.data_ptr(), self.num_pages,
                                stride(k_pages), stride(v_pages), stride(k_idx_pages), self.page_size, self.G, self.d,
                                self.d_idx)
+        self.address = ctypes.addressof(self.c)
+        self.workspaces = {}   # bytes that paged_decode needs, by the call's sizes
 
 
-def _table(page_table: torch.Tensor, seqlens: torch.Tensor, device, batch: int) -> None:
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != device \
-            or page_table.shape[0] != batch or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
-        raise ValueError(f"page_table must be int32 [{batch}, pages] on {device}, its rows contiguous")
-    _small(seqlens, "seqlens", device, torch.int32, (batch,))
-
-
-def _table_stride(page_table: torch.Tensor) -> int:
-    return max(page_table.stride(0), page_table.shape[1]) if page_table.shape[0] == 1 else page_table.stride(0)
+def _table(page_table: torch.Tensor, index: int, batch: int) -> tuple[int, int, int]:
+    """(address, columns, stride of rows) of a page table."""
+    shape, st = page_table.shape, page_table.stride()
+    if page_table.dtype != torch.int32 or len(shape) != 2 or page_table.get_device() != index or shape[0] != batch \
+            or (st[1] != 1 and shape[1] > 1):
+        raise ValueError(f"page_table must be int32 [{batch}, pages] on device {index}, its rows contiguous")
+    return page_table.data_ptr(), shape[1], max(st[0], shape[1]) if batch == 1 else st[0]
 
 
 def paged_append(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -495,37 +515,27 @@ def paged_append(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Ten
     says which rows are whose (None: N / B each); rows behind cu_seqlens[B] are padding. q [N, Hq, d] and
     q_idx [N, G, d_idx] are rotated in the same launch into q_out / q_idx_out (bf16; allocated if None,
     padding rows then undefined). Returns (q_out, q_idx_out)."""
-    lib = load_library()
-    device, dtype, n, batch = cache.device, k.dtype, k.shape[0], seqlens.shape[0]
+    index, dtype, n, batch = cache.index, k.dtype, k.shape[0], seqlens.shape[0]
     if dtype not in _DTYPES:
         raise ValueError(f"paged_append takes bfloat16, float16 and float32, not {dtype}")
-    _table(page_table, seqlens, device, batch)
-    _no_grad(k, v, k_idx, q, q_idx)
-    for t, name in ((k, "k"), (v, "v"), (k_idx, "k_idx"), (q, "q"), (q_idx, "q_idx")):
-        if t is not None:
-            _heads(t, name, n, device, dtype)
-    outs = []
-    for t, o, name in ((q, q_out, "q_out"), (q_idx, q_idx_out, "q_idx_out")):
-        if t is None and o is not None:
-            raise ValueError(f"{name} without its input")
-        if t is not None and o is None:
-            o = torch.empty(t.shape, dtype=torch.bfloat16, device=device)
-        elif t is not None:
-            _heads(o, name, n, device, torch.bfloat16)
-            if o.shape != t.shape:
-                raise ValueError(f"{name} must have its input's shape")
-        outs.append(o)
-    f, rot = (None, 0) if freqs is None else _freqs(freqs, "freqs", device)
-    fi, irot = (f, rot) if rotate_index else (None, 0)
+    table, columns, stride = _table(page_table, index, batch)
+    if (q is None and q_out is not None) or (q_idx is None and q_idx_out is not None):
+        raise ValueError("q_out or q_idx_out without its input")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if q_idx is not None and q_idx_out is None:
+        q_idx_out = torch.empty(q_idx.shape, dtype=torch.bfloat16, device=q_idx.device)
+    f, rot = (0, 0) if freqs is None else _freqs(freqs, "freqs", index)
+    fi, irot = (f, rot) if rotate_index else (0, 0)
     if idx_freqs is not None:
-        fi, irot = _freqs(idx_freqs, "idx_freqs", device)
-    cu = None if cu_seqlens is None else _small(cu_seqlens, "cu_seqlens", device, torch.int32, (batch + 1,))
-    p = MsaPagedAppendParams(_DTYPES[dtype], batch, page_table.shape[1], int(interleaved), rot, irot, rope_scale,
-                             _table_stride(page_table), page_table.data_ptr(), seqlens.data_ptr(), cu, f, fi)
-    _launch(device, lib.msa_paged_append, cache.c, p, _rope_tensor(k, None), _rope_tensor(v, None),
-            _rope_tensor(k_idx, None), None if q is None else _rope_tensor(q, outs[0]),
-            None if q_idx is None else _rope_tensor(q_idx, outs[1]), n)
-    return outs[0], outs[1]
+        fi, irot = _freqs(idx_freqs, "idx_freqs", index)
+    cu = 0 if cu_seqlens is None else _small(cu_seqlens, "cu_seqlens", index, torch.int32, (batch + 1,))
+    p = _PACK_APPEND(_DTYPES[dtype], batch, columns, bool(interleaved), rot, irot, rope_scale, stride, table,
+                     _small(seqlens, "seqlens", index, torch.int32, (batch,)), cu, f, fi)
+    _launch(index, _serving()[1], cache.address, p, _heads(k, "k", n, index, dtype), _heads(v, "v", n, index, dtype),
+            _heads(k_idx, "k_idx", n, index, dtype), None if q is None else _heads(q, "q", n, index, dtype, q_out, torch.bfloat16),
+            None if q_idx is None else _heads(q_idx, "q_idx", n, index, dtype, q_idx_out, torch.bfloat16), n)
+    return q_out, q_idx_out
 
 
 def paged_decode_workspace(cache: PagedCache, batch: int, max_pages: int, hq: int, topk: int, bk: int = 128,
@@ -547,33 +557,40 @@ def paged_decode(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Ten
     in the cache already (paged_append). page_table [B, pages], seqlens [B] int32. prefix_pages int32
     [n]: the first n pages of every sequence, where the batch shares a prefix; it is scored once for all.
     block_ids int32 [..., G, topk] takes the selection. Returns o, shaped as q; rows without a token are 0."""
-    lib = load_library()
-    device, shape = cache.device, q.shape
-    S = 1 if len(shape) == 3 else shape[1]
+    index, shape = cache.index, q.shape
     if len(shape) not in (3, 4) or shape[-1] != cache.d:
         raise ValueError(f"q must be [B, Hq, {cache.d}] or [B, tokens, Hq, {cache.d}]")
-    batch, lead, hq = shape[0], tuple(shape[:-2]), shape[-2]
-    _table(page_table, seqlens, device, batch)
-    _no_grad(q, q_idx)
-    qp = _small(q, "q", device, torch.bfloat16, tuple(shape))
-    qip = _small(q_idx, "q_idx", device, torch.bfloat16, lead + (cache.G, cache.d_idx))
-    idp = None if block_ids is None else _small(block_ids, "block_ids", device, torch.int32, lead + (cache.G, topk))
+    batch, hq = shape[0], shape[-2]
+    S = 1 if len(shape) == 3 else shape[1]
+    if torch.is_grad_enabled() and (q.requires_grad or q_idx.requires_grad):
+        raise ValueError("the result would carry no gradient; call this under torch.no_grad()")
+    table, columns, stride = _table(page_table, index, batch)
+    lens = _small(seqlens, "seqlens", index, torch.int32, (batch,))
+    bf16, lead = torch.bfloat16, shape[:-2]
+    qp = _small(q, "q", index, bf16, shape)
+    qip = _small(q_idx, "q_idx", index, bf16, lead + (cache.G, cache.d_idx))
+    idp = None if block_ids is None else _small(block_ids, "block_ids", index, torch.int32, lead + (cache.G, topk))
     if o is None:
         o = torch.empty_like(q)
-    op = _small(o, "o", device, torch.bfloat16, tuple(shape))
-    pp, shared = None, 0
+    op = _small(o, "o", index, bf16, shape)
+    pp, shared = 0, 0
     if prefix_pages is not None:
         shared = prefix_pages.shape[0]
-        pp = _small(prefix_pages, "prefix_pages", device, torch.int32, (shared,))
-    p = MsaPagedDecodeParams(hq, batch, S, bk, topk, page_table.shape[1], shared, scale, _table_stride(page_table),
-                             page_table.data_ptr(), seqlens.data_ptr(), pp)
-    need = lib.msa_paged_decode_workspace(cache.c, p)
-    if need == 0:
-        raise MsaError(2, lib.msa_last_error_detail().decode())
-    ws = _workspace(need, device, workspace)
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {device}")
-    _launch(device, lib.msa_paged_decode, cache.c, p, qp, qip, idp, op, ws.data_ptr(), ws.numel() * ws.element_size())
+        pp = _small(prefix_pages, "prefix_pages", index, torch.int32, (shared,))
+    p = _PACK_DECODE(hq, batch, S, bk, topk, columns, shared, scale, stride, table, lens, pp)
+    fns = _serving()
+    sizes = (batch, S, hq, columns, topk, bk)
+    need = cache.workspaces.get(sizes)
+    if need is None:
+        need = fns[2](cache.address, p)
+        if need == 0:
+            raise MsaError(2, load_library().msa_last_error_detail().decode())
+        cache.workspaces[sizes] = need
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on device {index}")
+    _launch(index, fns[3], cache.address, p, qp, qip, idp, op, workspace.data_ptr(), workspace.nbytes)
     return o
 
 
