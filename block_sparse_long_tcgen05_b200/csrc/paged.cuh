@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) paged_scan_kernel(const __gri
   const PageView& V = P.view;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gq = lane >> 2, tq = lane & 3;
+  grid_launch_dependents();
   // running total of every sequence's spans of 128 tokens
   int total = 0;
   for (int b0 = 0; b0 < V.batch; b0 += kScanThreads) {
@@ -166,6 +167,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) paged_scan_kernel(const __gri
       }
     }
   }
+  grid_wait();   // nothing here depends on a prefix scan before it, but what follows does on both
 }
 
 // ------------------------------------------------------------------------------------
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
   const int64_t row = rg / P.G;
   const int b = static_cast<int>(row / V.S), s = static_cast<int>(row % V.S);
   int32_t* out = P.block_ids + rg * P.k;
+  grid_launch_dependents();
   const int64_t pos = paged_length(V, b, kKidPagedTopk) - V.S + s;
   const int bl = pos >= 0 ? static_cast<int>(pos / P.bk) : -1;
   if (lane == 0) P.arrived[rg] = 0u;
@@ -199,8 +202,10 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
     for (int e = lane; e < P.width / 8; e += 32) reinterpret_cast<uint4*>(P.o + rg * P.width)[e] = make_uint4(0, 0, 0, 0);
   if (bl + 1 <= P.k) {
     if (lane < P.k) out[lane] = lane <= bl ? lane : -1;
+    grid_wait();
     return;
   }
+  grid_wait();
   const uint32_t* src = P.maxima + rg * P.nbmax;
   uint32_t carried = 0u, carried_id = 0xffffffffu;   // lane r: the r-th best so far (key 0: none)
   for (int c0 = 0; P.k > 1 && c0 < bl; c0 += 1024) {
@@ -383,6 +388,7 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, 2) paged_attn_kernel(con
   }
   const int64_t strips = static_cast<int64_t>(total) * P.G;
   const int64_t run = max(static_cast<int64_t>(kPagedAttnLeast), (strips + gridDim.x - 1) / gridDim.x);
+  grid_wait();   // so far only what the call was given has been read
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * run;
   const int64_t end = min(strips, begin + run);
 
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, 2) paged_attn_kernel(con
           for (int n = 0; n < D / 16; ++n)
 #pragma unroll
             for (int y = 0; y < 4; ++y) area[(2 * tq + (y & 1)) * C::kPitch + n * 16 + gq + 8 * (y >> 1)] = o[t][n][y];
-          if (gq < 2) *reinterpret_cast<float2*>(area + 8 * C::kPitch + 2 * (2 * tq + gq)) = make_float2(m[t][gq], l[t][gq]);
+          if (gq < 2) *reinterpret_cast<float2*>(area + 8 * C::kPitch + 2 * (2 * tq + gq)) = make_float2(gq ? m[t][1] : m[t][0], gq ? l[t][1] : l[t][0]);
         };
 #pragma unroll
         for (int step = 2; step > 0; step >>= 1) {

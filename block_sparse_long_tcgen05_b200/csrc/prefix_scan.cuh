@@ -43,7 +43,8 @@ struct PrefixCfg {
 constexpr int kPrefixThreads = 320;   // producer, issuer, two epilogue warpgroups
 
 template <int DI, int RT>
-__global__ void __launch_bounds__(kPrefixThreads, 1)
+// Few enough registers that a block of the sequences' own scan runs beside this one.
+__global__ void __launch_bounds__(kPrefixThreads, 2)
 prefix_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ PrefixScanParams P) {
   using C = PrefixCfg<DI, RT>;
@@ -61,6 +62,7 @@ prefix_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   WaitCtl* ctl = reinterpret_cast<WaitCtl*>(tmem_slot + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -208,22 +210,28 @@ prefix_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!mbar_wait(&acc_full[ab], static_cast<uint32_t>(ik / C::kBuffers) & 1, ctl, kKidPrefixScan)) { ok = false; break; }
         tc_fence_after();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (ab * RT + (RT == 1 ? 0 : group)) * 128;
-        uint32_t r[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(taddr + c * 32, r[c]);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[ab]);
         float m = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int half = 0; half < 2; ++half) {   // 64 columns at a time
+          uint32_t r[2][32];
+          tmem_ld32(taddr + half * 64, r[0]);
+          tmem_ld32(taddr + half * 64 + 32, r[1]);
+          tmem_ld_wait();
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[ab]);
+          }
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) m = max3f(m, __uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
-          if ((c + 1) * 32 % P.bk == 0) {
-            const int blk = t * F + (c * 32) / P.bk;
-            if (row < P.rows && blk < P.blocks) out[blk] = ordered_key(m);
-            m = -INFINITY;
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) m = max3f(m, __uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
+            const int done = (half * 2 + c + 1) * 32;
+            if (done % P.bk == 0) {
+              const int blk = t * F + done / P.bk - 1;
+              if (row < P.rows && blk < P.blocks) out[blk] = ordered_key(m);
+              m = -INFINITY;
+            }
           }
         }
       }

@@ -143,6 +143,26 @@ msa_status_t check_sequences(const msa_paged_cache* c, int32_t batch, int32_t ma
 // CTAs of the paged attention: two an SM are resident at once.
 int paged_attn_ctas() { return 2 * num_sms(); }
 
+// Launches a kernel of a decode; `after`: its blocks may start while the decode's kernel before it
+// still runs (each waits for it where it first needs its results). The first one of a call starts
+// when everything before it in the stream is done, as always.
+template <typename... Params, typename... Args>
+msa_status_t launch_step(void (*kernel)(Params...), int64_t grid, int threads, int smem, bool after, cudaStream_t st,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  MSA_CHECK_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+  return MSA_OK;
+}
+
 struct PagedLayout {
   uint32_t* maxima = nullptr;
   int32_t* block_ids = nullptr;
@@ -186,7 +206,7 @@ msa_status_t check_paged_shapes(const msa_paged_cache* c, const msa_paged_decode
 }
 
 template <int DI>
-msa_status_t launch_paged_scan(const PagedScanParams& P, cudaStream_t st) {
+msa_status_t launch_paged_scan(const PagedScanParams& P, bool after, cudaStream_t st) {
   static std::once_flag once;
   static int per_sm = 0;
   std::call_once(once, [] {
@@ -197,9 +217,7 @@ msa_status_t launch_paged_scan(const PagedScanParams& P, cudaStream_t st) {
   const int64_t most = int64_t(P.view.batch) * ((int64_t(P.nbmax) * P.bk + 127) / 128) * P.G;
   const int64_t grid = std::min<int64_t>(int64_t(num_sms()) * per_sm, (most + 7) / 8);
   ProfScope ps(kPPagedScan, st);
-  paged_scan_kernel<DI><<<unsigned(std::max<int64_t>(grid, 1)), kScanThreads, 0, st>>>(P);
-  MSA_CHECK_LAUNCH();
-  return MSA_OK;
+  return launch_step(paged_scan_kernel<DI>, std::max<int64_t>(grid, 1), kScanThreads, 0, after, st, P);
 }
 
 template <int DI, int RT>
@@ -214,9 +232,7 @@ msa_status_t launch_prefix_scan(const CUtensorMap& tq, const CUtensorMap& tk, Pr
   P.workers = std::max(1, std::min(sms / P.pairs, P.tiles));
   const int grid = P.workers > 1 ? P.workers * P.pairs : std::min(sms, P.pairs);
   ProfScope ps(kPPrefixScan, st);
-  prefix_scan_kernel<DI, RT><<<grid, kPrefixThreads, C::kSmemBytes, st>>>(tq, tk, P);
-  MSA_CHECK_LAUNCH();
-  return MSA_OK;
+  return launch_step(prefix_scan_kernel<DI, RT>, grid, kPrefixThreads, C::kSmemBytes, false, st, tq, tk, P);
 }
 
 template <int DI>
@@ -244,9 +260,7 @@ msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
   const int64_t most = int64_t(P.view.batch) * P.view.S * P.G * P.k * (P.bk / 16);   // strips
   const int64_t grid = std::min<int64_t>(paged_attn_ctas(), (most + kPagedAttnLeast - 1) / kPagedAttnLeast);
   ProfScope ps(kPPagedAttn, st);
-  paged_attn_kernel<D, NT><<<unsigned(grid), kPagedAttnWarps * 32, C::smem_bytes(P.view.batch), st>>>(P);
-  MSA_CHECK_LAUNCH();
-  return MSA_OK;
+  return launch_step(paged_attn_kernel<D, NT>, grid, kPagedAttnWarps * 32, C::smem_bytes(P.view.batch), true, st, P);
 }
 
 msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_params* p, const void* q, const void* q_idx,
@@ -266,6 +280,7 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
   const int nbmax = int(paged_blocks(c, p));
   int32_t* ids = block_ids_out ? block_ids_out : L.block_ids;
   msa_status_t s;
+  bool scanned = false;
   if (p->k > 1 && nbmax > p->k) {   // else every visible block is taken, or the local one alone
     PagedScanParams sp{};
     sp.view = V;
@@ -298,8 +313,10 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
         sp.nb0 = P.blocks;
       }
     }
-    s = c->d_idx == 128 ? launch_paged_scan<128>(sp, st) : c->d_idx == 64 ? launch_paged_scan<64>(sp, st) : launch_paged_scan<32>(sp, st);
+    s = c->d_idx == 128 ? launch_paged_scan<128>(sp, sp.nb0 > 0, st) : c->d_idx == 64 ? launch_paged_scan<64>(sp, sp.nb0 > 0, st)
+                                                                                   : launch_paged_scan<32>(sp, sp.nb0 > 0, st);
     if (s != MSA_OK) return s;
+    scanned = true;
   }
   PagedTopkParams tp{};
   tp.view = V;
@@ -315,9 +332,8 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
   const int64_t rg = int64_t(p->batch) * p->n_new * c->g;
   {
     ProfScope ps(kPPagedTopk, st);
-    paged_topk_kernel<<<unsigned((rg + 3) / 4), 128, 0, st>>>(tp);
+    if ((s = launch_step(paged_topk_kernel, (rg + 3) / 4, 128, 0, scanned, st, tp)) != MSA_OK) return s;
   }
-  MSA_CHECK_LAUNCH();
   PagedAttnParams ap{};
   ap.view = V;
   ap.q = static_cast<const __nv_bfloat16*>(q);
