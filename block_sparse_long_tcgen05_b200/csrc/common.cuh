@@ -35,6 +35,7 @@ enum KernelId : int {
   kKidPagedTopk = 11,
   kKidPagedAttn = 12,
   kKidPrefixScan = 13,
+  kKidPagedSmall = 14,
 };
 
 // Device error word: low byte = first msa_status_t recorded, next byte = kernel id.

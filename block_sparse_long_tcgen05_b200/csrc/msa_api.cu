@@ -22,6 +22,7 @@
 #include "merge.cuh"
 #include "decode.cuh"
 #include "paged.cuh"
+#include "paged_small.cuh"
 #include "prefix_scan.cuh"
 #include "rotate.cuh"
 #include "topk.cuh"
@@ -190,13 +191,13 @@ msa_status_t set_smem(K kernel, int bytes) {
 enum ProfKind {
   kPIndex, kPTopkPrefill, kPCsrCount, kPCsrScan, kPCsrOffsets, kPCsrScatter, kPCsrItems, kPKvOuter, kPMerge,
   kPDecodeScan, kPTopkDecode, kPDecodeAttn, kPIndexTopk, kPKl, kPKlMerge,
-  kPRotate, kPPagedScan, kPPagedTopk, kPPagedAttn, kPPrefixScan, kPNumKinds
+  kPRotate, kPPagedScan, kPPagedTopk, kPPagedAttn, kPPrefixScan, kPPagedSmall, kPNumKinds
 };
 const char* const kProfNames[kPNumKinds] = {"index_blockmax", "topk_prefill", "csr_count", "csr_scan",
                                             "csr_offsets", "csr_scatter", "csr_items", "kvouter", "merge",
                                             "decode_scan", "topk_decode", "decode_attn", "index_topk", "kl",
                                             "kl_merge", "rotate", "paged_scan", "paged_topk", "paged_attn",
-                                            "prefix_scan"};
+                                            "prefix_scan", "paged_small"};
 struct ProfRec {
   int kind;
   cudaEvent_t a, b;

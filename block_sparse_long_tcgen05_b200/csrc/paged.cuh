@@ -69,6 +69,36 @@ struct PagedScanParams {
 constexpr int kScanMaxBatch = 4096;
 constexpr int kScanThreads = 256;
 
+// Scores of 16 keys (rows gq and gq + 8 of `base`, at the lane's 16 bytes of every 64) against the queries
+// in qv, maxima with what m0, m1 hold of columns 2 tq and 2 tq + 1.
+template <int DI>
+__device__ __forceinline__ void scan_tile(const __nv_bfloat16* base, int64_t row, int gq, const uint4 (&qv)[DI / 32], float& m0,
+                                          float& m1) {
+  constexpr int CH = DI / 32;
+  uint4 x[CH], y[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    x[c] = __ldg(reinterpret_cast<const uint4*>(base + gq * row + c * 32));
+    y[c] = __ldg(reinterpret_cast<const uint4*>(base + (gq + 8) * row + c * 32));
+  }
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    mma_16816(acc, {x[c].x, y[c].x, x[c].y, y[c].y}, {qv[c].x, qv[c].y});
+    mma_16816(acc, {x[c].z, y[c].z, x[c].w, y[c].w}, {qv[c].z, qv[c].w});
+  }
+  m0 = max3f(m0, acc[0], acc[2]);
+  m1 = max3f(m1, acc[1], acc[3]);
+}
+// The maxima of the block, over the keys that other lanes hold.
+__device__ __forceinline__ void scan_block_max(float& m0, float& m1) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+}
+
 template <int DI>
 __global__ void __launch_bounds__(kScanThreads, 2) paged_scan_kernel(const __grid_constant__ PagedScanParams P) {
   constexpr int CH = DI / 32;
@@ -137,26 +167,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) paged_scan_kernel(const __gri
     for (int t = 0; t < tiles; ++t) {
       const int64_t page = __shfl_sync(0xffffffffu, my_page, (t << 4) >> V.shift);
       const __nv_bfloat16* base = P.pages + page * P.page_stride + ((token0 + t * 16) & mask) * row + g * DI + tq * 8;
-      uint4 x[CH], y[CH];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        x[c] = __ldg(reinterpret_cast<const uint4*>(base + gq * row + c * 32));
-        y[c] = __ldg(reinterpret_cast<const uint4*>(base + (gq + 8) * row + c * 32));
-      }
-      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        mma_16816(acc, {x[c].x, y[c].x, x[c].y, y[c].y}, {qv[c].x, qv[c].y});
-        mma_16816(acc, {x[c].z, y[c].z, x[c].w, y[c].w}, {qv[c].z, qv[c].w});
-      }
-      m0 = max3f(m0, acc[0], acc[2]);
-      m1 = max3f(m1, acc[1], acc[3]);
+      scan_tile<DI>(base, row, gq, qv, m0, m1);
       if ((t + 1) % tiles_of_block == 0) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-        }
+        scan_block_max(m0, m1);
         const int blk = static_cast<int>((token0 + t * 16) / P.bk);
         if (gq == 0) {
           uint32_t* out = P.maxima + ((static_cast<int64_t>(b) * V.S + 2 * tq) * P.G + g) * P.nbmax + blk;
@@ -186,36 +199,18 @@ struct PagedTopkParams {
   int G, bk, k, nbmax, width;
 };
 
-__global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__ PagedTopkParams P) {
-  const PageView& V = P.view;
-  const int64_t rg = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (rg >= static_cast<int64_t>(V.batch) * V.S * P.G) return;
-  const int64_t row = rg / P.G;
-  const int b = static_cast<int>(row / V.S), s = static_cast<int>(row % V.S);
-  int32_t* out = P.block_ids + rg * P.k;
-  grid_launch_dependents();
-  const int64_t pos = paged_length(V, b, kKidPagedTopk) - V.S + s;
-  const int bl = pos >= 0 ? static_cast<int>(pos / P.bk) : -1;
-  if (lane == 0) P.arrived[rg] = 0u;
-  if (bl < 0)
-    for (int e = lane; e < P.width / 8; e += 32) reinterpret_cast<uint4*>(P.o + rg * P.width)[e] = make_uint4(0, 0, 0, 0);
-  if (bl + 1 <= P.k) {
-    if (lane < P.k) out[lane] = lane <= bl ? lane : -1;
-    grid_wait();
-    return;
-  }
-  grid_wait();
-  const uint32_t* src = P.maxima + rg * P.nbmax;
+// The k - 1 best of the keys src[0 .. n), n >= k - 1, of one warp: lane r < k - 1 returns the r-th
+// best one's id, and in `place` its place among them in ascending order of ids.
+__device__ __forceinline__ int topk_warp(const uint32_t* src, int n, int k, int lane, int& place) {
   uint32_t carried = 0u, carried_id = 0xffffffffu;   // lane r: the r-th best so far (key 0: none)
-  for (int c0 = 0; P.k > 1 && c0 < bl; c0 += 1024) {
+  for (int c0 = 0; k > 1 && c0 < n; c0 += 1024) {
     uint32_t key[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) key[j] = c0 + j * 32 + lane < bl ? __ldg(src + c0 + j * 32 + lane) : 0u;
+    for (int j = 0; j < 32; ++j) key[j] = c0 + j * 32 + lane < n ? src[c0 + j * 32 + lane] : 0u;
     uint32_t next = 0u, next_id = 0xffffffffu;
     uint32_t best = 0u;
     int at = -1;
-    for (int r = 0; r + 1 < P.k; ++r) {
+    for (int r = 0; r + 1 < k; ++r) {
       best = carried;
       at = -1;
 #pragma unroll
@@ -237,9 +232,35 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
     carried_id = next_id;
   }
   // ascending: an id's place is the number of smaller ones
-  int place = 0;
-  for (int r = 0; r + 1 < P.k; ++r) place += __shfl_sync(0xffffffffu, carried_id, r) < carried_id;
-  if (lane + 1 < P.k) out[place] = static_cast<int32_t>(carried_id);
+  place = 0;
+  for (int r = 0; r + 1 < k; ++r) place += __shfl_sync(0xffffffffu, carried_id, r) < carried_id;
+  return static_cast<int>(carried_id);
+}
+
+__global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__ PagedTopkParams P) {
+  const PageView& V = P.view;
+  const int64_t rg = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (rg >= static_cast<int64_t>(V.batch) * V.S * P.G) return;
+  const int64_t row = rg / P.G;
+  const int b = static_cast<int>(row / V.S), s = static_cast<int>(row % V.S);
+  int32_t* out = P.block_ids + rg * P.k;
+  grid_launch_dependents();
+  const int64_t pos = paged_length(V, b, kKidPagedTopk) - V.S + s;
+  const int bl = pos >= 0 ? static_cast<int>(pos / P.bk) : -1;
+  if (lane == 0) P.arrived[rg] = 0u;
+  if (bl < 0)
+    for (int e = lane; e < P.width / 8; e += 32) reinterpret_cast<uint4*>(P.o + rg * P.width)[e] = make_uint4(0, 0, 0, 0);
+  if (bl + 1 <= P.k) {
+    if (lane < P.k) out[lane] = lane <= bl ? lane : -1;
+    grid_wait();
+    return;
+  }
+  grid_wait();
+  const uint32_t* src = P.maxima + rg * P.nbmax;
+  int place;
+  const int id = topk_warp(src, bl, P.k, lane, place);
+  if (lane + 1 < P.k) out[place] = id;
   if (lane == 0) out[P.k - 1] = bl;
 }
 
@@ -271,19 +292,24 @@ struct PagedAttnParams {
   __nv_bfloat16* o;            // [batch][S][G * R][D]
   float* parts;                // [2 * CTAs][R][D + 2]: O, then m and l; part 2 c continues a unit, 2 c + 1 begins one
   unsigned int* arrived;       // [rows][G] parts written so far (zeroed by the Top-k)
-  int G, R, k, bk;
+  int G, R, k, bk_shift;       // blocks of 1 << bk_shift tokens
   float scale_log2;
 };
 
 constexpr int kPagedAttnWarps = 4;
-constexpr int kPagedAttnTable = 512;   // strips looked up at a time
-constexpr int kPagedAttnRing = 2;
+constexpr int kPagedAttnTable = 256;   // strips looked up at a time
+constexpr int kPagedAttnRing = 2;      // strips' values a warp has room for
 constexpr int kPagedAttnLeast = 16;    // strips of a run, where there are enough: shorter ones cost more to join than they save
+// CTAs resident on an SM. Three of 168 registers a thread: two take 7% longer (16 x 4 drafted tokens behind
+// 32K), four of 128 registers spill and take 5% longer.
+constexpr int kPagedAttnCtas(int nt) { return nt == 1 ? 3 : 2; }
 template <int D>
 struct PagedAttnCfg {
-  static constexpr int kStrip = 2 * 16 * D;                  // elements of a strip's K and V
-  static constexpr int kPitch = D + 4;                       // of a head's O: the lanes' stores hit distinct banks
+  static constexpr int kStrip = 16 * D;                      // elements of a strip's values
+  static constexpr int kPitch = D + 4;                       // of a head's O in the join
   static constexpr int kEight = 8 * kPitch + 16;             // floats of 8 heads' O, m and l
+  // shares of at most 18 parts (a unit has up to 256 strips, a run at least 16) of 16 heads
+  static_assert(2 * kEight * 4 >= 18 * 16 * 8, "the shares fit the join's memory");
   static constexpr int kJoinOff = kPagedAttnWarps * kPagedAttnRing * kStrip * 2;
   static constexpr int kTableOff = kJoinOff + 2 * kEight * 4;
   static constexpr int kEndsOff = kTableOff + kPagedAttnTable * 8;
@@ -310,23 +336,138 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return y;
 }
 
+// S^T of a strip: keys kx, ky as they lie (rows gq and gq + 8), queries qf in the same order of elements;
+// two sums whose chains are shorter.
+template <int D, int NT>
+__device__ __forceinline__ void strip_scores(const uint4 (&kx)[D / 32], const uint4 (&ky)[D / 32], const uint4 (&qf)[NT][D / 32],
+                                             float (&sc)[NT][2][4]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) sc[t][0][y] = sc[t][1][y] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      mma_16816(sc[t][0], {kx[c].x, ky[c].x, kx[c].y, ky[c].y}, {qf[t][c].x, qf[t][c].y});
+      mma_16816(sc[t][1], {kx[c].z, ky[c].z, kx[c].w, ky[c].w}, {qf[t][c].z, qf[t][c].w});
+    }
+}
+
+// The strip's softmax against the running maximum and sum (m, l: heads 8 t + 2 tq and the next; the sum is
+// of this lane's tokens), its weights P^T as an operand; nv: tokens that count.
+template <int D, int NT>
+__device__ __forceinline__ void strip_softmax(const float (&sc)[NT][2][4], int nv, float scale_log2, int gq, float (&m)[NT][2],
+                                              float (&l)[NT][2], float (&o)[NT][D / 16][4], uint32_t (&pf)[NT][2]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float x[4], top[2] = {m[t][0], m[t][1]};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      x[y] = gq + 8 * (y >> 1) < nv ? (sc[t][0][y] + sc[t][1][y]) * scale_log2 : -INFINITY;
+      top[y & 1] = fmaxf(top[y & 1], x[y]);
+    }
+    float keep[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], off));
+      const float from = top[h] == -INFINITY ? 0.0f : top[h];   // every score so far is -inf
+      keep[h] = exp2f(m[t][h] - from);
+      m[t][h] = top[h];
+      top[h] = from;
+      l[t][h] *= keep[h];
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      x[y] = exp2f(x[y] - top[y & 1]);
+      l[t][y & 1] += x[y];
+    }
+    pf[t][0] = transpose_8x8(pack_bf16x2(x[0], x[1]));
+    pf[t][1] = transpose_8x8(pack_bf16x2(x[2], x[3]));
+    if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[t][n][y] *= keep[y & 1];
+    }
+  }
+}
+
+// O^T += V^T P^T: the strip's values in shared memory, 16-byte pieces c of row r at c ^ (r % 8).
+template <int D, int NT>
+__device__ __forceinline__ void strip_values(const __nv_bfloat16* vs, int lane, const uint32_t (&pf)[NT][2], float (&o)[NT][D / 16][4]) {
+  const int vr = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+  for (int n = 0; n < D / 16; ++n) {
+    uint32_t af[4];
+    ldsm_x4_trans(af, vs + vr * D + (((n * 2 + ((lane >> 3) & 1)) ^ (vr & 7)) * 8));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) mma_16816(o[t][n], af, pf[t]);
+  }
+}
+
+// The four warps' results for eight heads into `join` (head h: O at h * pitch, maximum and sum behind the
+// eight): warps 2 and 3 into 0 and 1, 1 into 0, that out. Ends with a barrier; two areas of 8 * pitch + 16.
+template <int D>
+__device__ __forceinline__ void join_warps(float (&o)[D / 16][4], float (&m)[2], float (&l)[2], float* join, int warp, int gq, int tq) {
+  constexpr int kPitch = D + 4;   // the lanes' stores hit distinct banks
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
+  auto put = [&](float* area) {
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) area[(2 * tq + (y & 1)) * kPitch + n * 16 + gq + 8 * (y >> 1)] = o[n][y];
+    if (gq < 2) *reinterpret_cast<float2*>(area + 8 * kPitch + 2 * (2 * tq + gq)) = make_float2(gq ? m[1] : m[0], gq ? l[1] : l[0]);
+  };
+#pragma unroll
+  for (int step = 2; step > 0; step >>= 1) {
+    float* area = join + (step == 2 ? warp & 1 : 0) * (8 * kPitch + 16);
+    if (warp >= step && warp < 2 * step) put(area);
+    __syncthreads();
+    if (warp < step) {
+      float mine[2], theirs[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 ml = *reinterpret_cast<const float2*>(area + 8 * kPitch + 2 * (2 * tq + h));
+        const float top = fmaxf(m[h], ml.x);
+        mine[h] = m[h] == -INFINITY ? 0.0f : exp2f(m[h] - top);   // 0: a warp without a token
+        theirs[h] = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+        m[h] = top;
+        l[h] = l[h] * mine[h] + ml.y * theirs[h];
+      }
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          o[n][y] = o[n][y] * mine[y & 1] + area[(2 * tq + (y & 1)) * kPitch + n * 16 + gq + 8 * (y >> 1)] * theirs[y & 1];
+    }
+    __syncthreads();
+  }
+  if (warp == 0) put(join);
+  __syncthreads();
+}
+
 // A place in the list of strips: strip `at` of the `n` strips of (sequence b, new token s, group g);
-// `unit` is the first of them in the list.
+// `unit` is the first of them in the list. The list has fewer than 2^31 strips (4096 sequences of 8 new
+// tokens, 64 groups, 256 strips), so 32 bits do: 64-bit divisions took microseconds here.
 struct StripPlace {
-  int b, s, g, n, at;
-  int64_t pos, unit;
+  int b, s, g, n, at, unit, pos;
 };
 
-// Strips of one group of new token s of a sequence of length L.
-__device__ __forceinline__ int row_strips(int64_t L, int S, int s, int k, int bk) {
-  const int64_t pos = L - S + s;
-  return pos < 0 ? 0 : min(k, static_cast<int>(pos / bk) + 1) * (bk >> 4);
+// Strips of one group of new token s of a sequence of length L; blocks of 1 << bk_shift tokens.
+__device__ __forceinline__ int row_strips(int L, int S, int s, int k, int bk_shift) {
+  const int pos = L - S + s;
+  return pos < 0 ? 0 : min(k, (pos >> bk_shift) + 1) << (bk_shift - 4);
 }
 
 // ends[b]: strips of sequences 0 .. b, divided by G.
-__device__ __forceinline__ StripPlace find_strip(const PagedAttnParams& P, const int* ends, int64_t t) {
+__device__ __forceinline__ StripPlace find_strip(const PagedAttnParams& P, const int* ends, int t) {
   const PageView& V = P.view;
-  const int tg = static_cast<int>(t / P.G);   // a sequence's strips are a multiple of G
+  const int tg = static_cast<uint32_t>(t) / static_cast<uint32_t>(P.G);   // a sequence's strips are a multiple of G
   int lo = 0, hi = V.batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -334,23 +475,23 @@ __device__ __forceinline__ StripPlace find_strip(const PagedAttnParams& P, const
   }
   StripPlace x;
   x.b = lo;
-  const int64_t L = V.seqlens[lo];
-  x.unit = lo > 0 ? static_cast<int64_t>(ends[lo - 1]) * P.G : 0;
+  const int L = V.seqlens[lo];
+  x.unit = lo > 0 ? ends[lo - 1] * P.G : 0;
   for (x.s = 0;; ++x.s) {
-    x.n = row_strips(L, V.S, x.s, P.k, P.bk);
-    if (t < x.unit + static_cast<int64_t>(x.n) * P.G || x.s + 1 == V.S) break;
-    x.unit += static_cast<int64_t>(x.n) * P.G;
+    x.n = row_strips(L, V.S, x.s, P.k, P.bk_shift);
+    if (t < x.unit + x.n * P.G || x.s + 1 == V.S) break;
+    x.unit += x.n * P.G;
   }
-  x.g = static_cast<int>((t - x.unit) / x.n);
-  x.unit += static_cast<int64_t>(x.g) * x.n;
-  x.at = static_cast<int>(t - x.unit);
+  x.g = static_cast<uint32_t>(t - x.unit) / static_cast<uint32_t>(x.n);
+  x.unit += x.g * x.n;
+  x.at = t - x.unit;
   x.pos = L - V.S + x.s;
   return x;
 }
 
 // NT: tiles of 8 heads.
 template <int D, int NT>
-__global__ void __launch_bounds__(kPagedAttnWarps * 32, 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
+__global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) paged_attn_kernel(const __grid_constant__ PagedAttnParams P) {
   using C = PagedAttnCfg<D>;
   constexpr int kThreads = kPagedAttnWarps * 32;
   extern __shared__ __align__(16) uint8_t psm[];
@@ -368,8 +509,8 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, 2) paged_attn_kernel(con
     const int b = b0 + threadIdx.x;
     int x = 0;
     if (b < V.batch) {
-      const int64_t L = paged_length(V, b, kKidPagedAttn);
-      for (int s = 0; L > 0 && s < V.S; ++s) x += row_strips(L, V.S, s, P.k, P.bk);
+      const int L = static_cast<int>(paged_length(V, b, kKidPagedAttn));
+      for (int s = 0; L > 0 && s < V.S; ++s) x += row_strips(L, V.S, s, P.k, P.bk_shift);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -386,196 +527,121 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, 2) paged_attn_kernel(con
     if (b < V.batch) ends[b] = before + x;
     __syncthreads();
   }
-  const int64_t strips = static_cast<int64_t>(total) * P.G;
-  const int64_t run = max(static_cast<int64_t>(kPagedAttnLeast), (strips + gridDim.x - 1) / gridDim.x);
+  const int strips = total * P.G;
+  const int run = max(kPagedAttnLeast, static_cast<int>((strips + gridDim.x - 1u) / gridDim.x));
   grid_wait();   // so far only what the call was given has been read
-  const int64_t begin = static_cast<int64_t>(blockIdx.x) * run;
-  const int64_t end = min(strips, begin + run);
+  // (the last CTA's run may begin behind the list's end, by less than run * CTAs: no more than 2^31)
+  const int begin = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * run, static_cast<int64_t>(strips)));
+  const int end = min(strips, begin + min(run, strips));
 
   __nv_bfloat16* ring = reinterpret_cast<__nv_bfloat16*>(psm) + warp * kPagedAttnRing * C::kStrip;
   const int64_t row = static_cast<int64_t>(P.G) * D;
-  // starts the copies of entry i of the table
-  auto fetch = [&](int i, int count, int stage) {
+  // starts the copies of the values of entry i of the table
+  auto fetch_v = [&](int i, int count, int stage) {
     if (i < count) {
       const int2 at = table[i];
       const int seen = at.y & 31;
       if (seen > 0) {
-        const int64_t off = static_cast<int64_t>(at.y >> 16) * row + ((at.y >> 8) & 255) * D;
-        const __nv_bfloat16* ks = P.kp + at.x * P.k_stride + off;
-        const __nv_bfloat16* vs = P.vp + at.x * P.v_stride + off;
-        __nv_bfloat16* kd = ring + stage * C::kStrip;
-        __nv_bfloat16* vd = kd + 16 * D;
+        const __nv_bfloat16* vs = P.vp + at.x * P.v_stride + static_cast<int64_t>(at.y >> 16) * row + ((at.y >> 8) & 255) * D;
+        __nv_bfloat16* vd = ring + stage * C::kStrip;
 #pragma unroll
         for (int e = lane; e < 16 * (D / 8); e += 32) {
           const int r = e / (D / 8), c = e % (D / 8);
           const bool ok = r < seen;   // rows behind the position read as zeros, whatever lies there
-          const int64_t so = ok ? r * row + c * 8 : 0;
-          const int to = r * D + ((c ^ (r & 7)) * 8);   // swizzled: ldmatrix rows hit distinct banks
-          cp_async16(kd + to, ks + so, ok);
-          cp_async16(vd + to, vs + so, ok);
+          cp_async16(vd + r * D + ((c ^ (r & 7)) * 8), vs + (ok ? r * row + c * 8 : 0), ok);   // swizzled for ldmatrix
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // the keys of entry i, as they lie: bytes 16 tq .. of every 64 of rows gq and gq + 8 (rows behind the
+  // position hold anything; they are masked as scores)
+  uint4 kx[D / 32], ky[D / 32];
+  auto fetch_k = [&](int i, int count) {
+    if (i < count) {
+      const int2 at = table[i];
+      if ((at.y & 31) > 0) {
+        const __nv_bfloat16* ks = P.kp + at.x * P.k_stride + static_cast<int64_t>((at.y >> 16) + gq) * row + ((at.y >> 8) & 255) * D + tq * 8;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          kx[c] = __ldg(reinterpret_cast<const uint4*>(ks + c * 32));
+          ky[c] = __ldg(reinterpret_cast<const uint4*>(ks + 8 * row + c * 32));
+        }
+      }
+    }
+  };
 
-  uint32_t qf[NT][D / 16][2];
+  uint4 qf[NT][D / 32];       // heads' queries, their elements in the keys' order
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2];   // heads 8 t + 2 tq and the next
   bool begun = false;   // the unit's registers hold strips of an earlier table
-  for (int64_t sub = begin; sub < end; sub += kPagedAttnTable) {
-    const int count = static_cast<int>(min(static_cast<int64_t>(kPagedAttnTable), end - sub));
+  for (int sub = begin; sub < end; sub += kPagedAttnTable) {
+    const int count = min(kPagedAttnTable, end - sub);
     for (int i = threadIdx.x; i < count; i += kThreads) {
       const StripPlace x = find_strip(P, ends, sub + i);
-      const int per_block = P.bk >> 4;
-      const int blk = __ldg(P.block_ids + ((static_cast<int64_t>(x.b) * V.S + x.s) * P.G + x.g) * P.k + x.at / per_block);
-      const int64_t t0 = static_cast<int64_t>(blk) * P.bk + (x.at % per_block) * 16;
-      int64_t page = -1;
-      if (blk >= 0 && t0 <= x.pos) page = page_of(V, x.b, t0, kKidPagedAttn);
-      const int seen = page >= 0 ? static_cast<int>(min(static_cast<int64_t>(16), x.pos - t0 + 1)) : 0;
-      table[i] = make_int2(static_cast<int>(page),
-                           (static_cast<int>(t0) & ((1 << V.shift) - 1)) << 16 | x.g << 8 | seen);
+      const int per_shift = P.bk_shift - 4;
+      const int blk = __ldg(P.block_ids + ((static_cast<int64_t>(x.b) * V.S + x.s) * P.G + x.g) * P.k + (x.at >> per_shift));
+      const int t0 = (blk << P.bk_shift) + ((x.at & ((1 << per_shift) - 1)) << 4);
+      int page = -1;
+      if (blk >= 0 && t0 <= x.pos) page = static_cast<int>(page_of(V, x.b, t0, kKidPagedAttn));
+      const int seen = page >= 0 ? min(16, x.pos - t0 + 1) : 0;
+      table[i] = make_int2(page, (t0 & ((1 << V.shift) - 1)) << 16 | x.g << 8 | seen);
     }
     __syncthreads();
     int i = warp, stage = 0;
 #pragma unroll
-    for (int st = 0; st < kPagedAttnRing - 1; ++st) fetch(warp + st * kPagedAttnWarps, count, st);
+    for (int st = 0; st < kPagedAttnRing - 1; ++st) fetch_v(warp + st * kPagedAttnWarps, count, st);
+    fetch_k(warp, count);
     for (int cur = 0; cur < count;) {
       const StripPlace x = find_strip(P, ends, sub + cur);
-      const int stop = static_cast<int>(min(static_cast<int64_t>(count), x.unit + x.n - sub));
+      const int stop = min(count, x.unit + x.n - sub);
       const int64_t rg = (static_cast<int64_t>(x.b) * V.S + x.s) * P.G + x.g;
       const int64_t head0 = rg * P.R;
       if (!begun) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int r = t * 8 + gq;
-          const uint32_t* q0 = reinterpret_cast<const uint32_t*>(P.q + (head0 + r) * D);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            qf[t][kk][0] = r < P.R ? __ldg(q0 + kk * 8 + tq) : 0u;
-            qf[t][kk][1] = r < P.R ? __ldg(q0 + kk * 8 + 4 + tq) : 0u;
+          for (int c = 0; c < D / 32; ++c)
+            qf[t][c] = r < P.R ? __ldg(reinterpret_cast<const uint4*>(P.q + (head0 + r) * D + c * 32 + tq * 8)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) o[t][kk][y] = 0.0f;
-          }
+          for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[t][n][y] = 0.0f;
           m[t][0] = m[t][1] = -INFINITY;
           l[t][0] = l[t][1] = 0.0f;
         }
       }
       for (; i < stop; i += kPagedAttnWarps) {
         __syncwarp();   // every lane is done with the stage that is refilled now
-        fetch(i + (kPagedAttnRing - 1) * kPagedAttnWarps, count, stage == 0 ? kPagedAttnRing - 1 : stage - 1);
+        fetch_v(i + (kPagedAttnRing - 1) * kPagedAttnWarps, count, stage == 0 ? kPagedAttnRing - 1 : stage - 1);
+        const int nv = table[i].y & 31;
+        const __nv_bfloat16* vs = ring + stage * C::kStrip;
+        stage = stage + 1 == kPagedAttnRing ? 0 : stage + 1;
+        if (nv == 0) {
+          fetch_k(i + kPagedAttnWarps, count);
+          continue;
+        }
+        float sc[NT][2][4];
+        strip_scores<D, NT>(kx, ky, qf, sc);
+        fetch_k(i + kPagedAttnWarps, count);   // under this strip's softmax and values
+        uint32_t pf[NT][2];
+        strip_softmax<D, NT>(sc, nv, P.scale_log2, gq, m, l, o, pf);
         asm volatile("cp.async.wait_group %0;" ::"n"(kPagedAttnRing - 1) : "memory");
         __syncwarp();
-        const int nv = table[i].y & 31;
-        const __nv_bfloat16* ks = ring + stage * C::kStrip;
-        const __nv_bfloat16* vs = ks + 16 * D;
-        stage = stage + 1 == kPagedAttnRing ? 0 : stage + 1;
-        if (nv == 0) continue;
-        // S^T: even and odd steps apart, two shorter chains
-        float sc[NT][2][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) sc[t][0][y] = sc[t][1][y] = 0.0f;
-        const int kr = lane & 15;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t af[4];
-          ldsm_x4(af, ks + kr * D + (((kk * 2 + (lane >> 4)) ^ (kr & 7)) * 8));
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_16816(sc[t][kk & 1], af, qf[t][kk]);
-        }
-        uint32_t pf[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float x[4], top[2] = {m[t][0], m[t][1]};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            x[y] = gq + 8 * (y >> 1) < nv ? (sc[t][0][y] + sc[t][1][y]) * P.scale_log2 : -INFINITY;
-            top[y & 1] = fmaxf(top[y & 1], x[y]);
-          }
-          float keep[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], off));
-            const float from = top[h] == -INFINITY ? 0.0f : top[h];   // every score so far is -inf
-            keep[h] = exp2f(m[t][h] - from);
-            m[t][h] = top[h];
-            top[h] = from;
-            l[t][h] *= keep[h];
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            x[y] = exp2f(x[y] - top[y & 1]);
-            l[t][y & 1] += x[y];
-          }
-          pf[t][0] = transpose_8x8(pack_bf16x2(x[0], x[1]));
-          pf[t][1] = transpose_8x8(pack_bf16x2(x[2], x[3]));
-          if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
-#pragma unroll
-            for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) o[t][n][y] *= keep[y & 1];
-          }
-        }
-        const int vr = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t af[4];
-          ldsm_x4_trans(af, vs + vr * D + (((n * 2 + ((lane >> 3) & 1)) ^ (vr & 7)) * 8));
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_16816(o[t][n], af, pf[t]);
-        }
+        strip_values<D, NT>(vs, lane, pf, o);
       }
       cur = stop;
       begun = sub + cur < x.unit + x.n && sub + cur < end;   // the next table goes on with this unit
       if (begun) continue;
 
-      // the warps' results, eight heads at a time: warps 2 and 3 into 0 and 1, 1 into 0, that out
-      const int64_t first_cta = x.unit / run, last_cta = (x.unit + x.n - 1) / run;
+      // the warps' results, eight heads at a time
+      const int first_cta = x.unit / run, last_cta = (x.unit + x.n - 1) / run;
       const bool whole = first_cta == last_cta;
       float* part = P.parts + (2 * static_cast<int64_t>(blockIdx.x) + (first_cta == blockIdx.x ? 1 : 0)) * P.R * (D + 2);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], off);
-        auto put = [&](float* area) {
-#pragma unroll
-          for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) area[(2 * tq + (y & 1)) * C::kPitch + n * 16 + gq + 8 * (y >> 1)] = o[t][n][y];
-          if (gq < 2) *reinterpret_cast<float2*>(area + 8 * C::kPitch + 2 * (2 * tq + gq)) = make_float2(gq ? m[t][1] : m[t][0], gq ? l[t][1] : l[t][0]);
-        };
-#pragma unroll
-        for (int step = 2; step > 0; step >>= 1) {
-          float* area = join + (step == 2 ? warp & 1 : 0) * C::kEight;
-          if (warp >= step && warp < 2 * step) put(area);
-          __syncthreads();
-          if (warp < step) {
-            float mine[2], theirs[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float2 ml = *reinterpret_cast<const float2*>(area + 8 * C::kPitch + 2 * (2 * tq + h));
-              const float top = fmaxf(m[t][h], ml.x);
-              mine[h] = m[t][h] == -INFINITY ? 0.0f : exp2f(m[t][h] - top);   // 0: a warp without a token
-              theirs[h] = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
-              m[t][h] = top;
-              l[t][h] = l[t][h] * mine[h] + ml.y * theirs[h];
-            }
-#pragma unroll
-            for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                o[t][n][y] = o[t][n][y] * mine[y & 1] +
-                             area[(2 * tq + (y & 1)) * C::kPitch + n * 16 + gq + 8 * (y >> 1)] * theirs[y & 1];
-          }
-          __syncthreads();
-        }
-        if (warp == 0) put(join);
-        __syncthreads();
+        join_warps<D>(o[t], m[t], l[t], join, warp, gq, tq);
         for (int e = threadIdx.x; e < 8 * (D / 2); e += kThreads) {
           const int r8 = e / (D / 2), c = (e % (D / 2)) * 2, r = t * 8 + r8;
           if (r >= P.R) break;
@@ -599,22 +665,50 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, 2) paged_attn_kernel(con
       __syncthreads();
       if (is_last) {
         __threadfence();
-        for (int e = threadIdx.x; e < P.R * (D / 2); e += kThreads) {
-          const int r = e / (D / 2), c = (e % (D / 2)) * 2;
-          float top = -INFINITY, sum = 0.0f, u = 0.0f, v = 0.0f;
-          for (int64_t w = first_cta; w <= last_cta; ++w) {
-            const float* from = P.parts + (2 * w + (w == first_cta ? 1 : 0)) * P.R * (D + 2);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + P.R * D + 2 * r));
-            const float2 ov = __ldcg(reinterpret_cast<const float2*>(from + r * D + c));
-            const float higher = fmaxf(top, ml.x);
-            const float a = top == -INFINITY ? 0.0f : exp2f(top - higher), f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - higher);
-            top = higher;
-            sum = sum * a + ml.y * f;
-            u = u * a + ov.x * f;
-            v = v * a + ov.y * f;
+        // every part's share of each head: 2^(its maximum - the common one), over the common sum
+        const int n_parts = last_cta - first_cta + 1;
+        auto part_of = [&](int w) { return P.parts + (2 * static_cast<int64_t>(first_cta + w) + (w == 0 ? 1 : 0)) * P.R * (D + 2); };
+        float2* share = reinterpret_cast<float2*>(join);   // [parts][R], then .x the share
+        for (int e = threadIdx.x; e < n_parts * P.R; e += kThreads) {
+          const int w = e / P.R;
+          share[e] = __ldcg(reinterpret_cast<const float2*>(part_of(w) + P.R * D) + e - w * P.R);
+        }
+        __syncthreads();
+        if (threadIdx.x < P.R) {
+          float top = -INFINITY, sum = 0.0f;
+          for (int w = 0; w < n_parts; ++w) top = fmaxf(top, share[w * P.R + threadIdx.x].x);
+          for (int w = 0; w < n_parts; ++w) {
+            float2& ml = share[w * P.R + threadIdx.x];
+            ml.x = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+            sum += ml.x * ml.y;
           }
           const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-          *reinterpret_cast<uint32_t*>(P.o + (head0 + r) * D + c) = pack_bf16x2(u * inv, v * inv);
+          for (int w = 0; w < n_parts; ++w) share[w * P.R + threadIdx.x].x *= inv;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < P.R * (D / 4); e += kThreads) {
+          const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+          float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int w0 = 0; w0 < n_parts; w0 += 4) {   // four parts' loads in flight
+            float2 lo[4], hi[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (w0 + w < n_parts) {
+                const float* from = part_of(w0 + w) + r * D + c;
+                lo[w] = __ldcg(reinterpret_cast<const float2*>(from));
+                hi[w] = __ldcg(reinterpret_cast<const float2*>(from + 2));
+              }
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (w0 + w < n_parts) {
+                const float f = share[(w0 + w) * P.R + r].x;
+                a[0] += f * lo[w].x;
+                a[1] += f * lo[w].y;
+                a[2] += f * hi[w].x;
+                a[3] += f * hi[w].y;
+              }
+          }
+          *reinterpret_cast<uint2*>(P.o + (head0 + r) * D + c) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
         }
       }
       __syncthreads();   // is_last is written again by the next unit

@@ -1,3 +1,9 @@
+#ifndef SMC
+#define SMC 2
+#endif
+#ifndef SMB
+#define SMB (1<<20)
+#endif
 // Host side of the serving entry points (rotary positions, paged append, paged decode): their
 // argument checks, workspace layout and launches. Included by msa_api.cu after its helpers.
 #pragma once
@@ -140,8 +146,8 @@ msa_status_t check_sequences(const msa_paged_cache* c, int32_t batch, int32_t ma
   return MSA_OK;
 }
 
-// CTAs of the paged attention: two an SM are resident at once.
-int paged_attn_ctas() { return 2 * num_sms(); }
+// CTAs of the paged attention: as many as are resident at once.
+int paged_attn_ctas(int R) { return kPagedAttnCtas(R <= 8 ? 1 : 2) * num_sms(); }
 
 // Launches a kernel of a decode; `after`: its blocks may start while the decode's kernel before it
 // still runs (each waits for it where it first needs its results). The first one of a call starts
@@ -181,7 +187,7 @@ PagedLayout paged_layout(void* ws, const msa_paged_cache* c, const msa_paged_dec
   PagedLayout L;
   L.maxima = static_cast<uint32_t*>(cv.take(size_t(rows) * c->g * paged_blocks(c, p) * 4));
   L.block_ids = static_cast<int32_t*>(cv.take(size_t(rows) * c->g * p->k * 4));   // used when the caller takes none
-  L.parts = static_cast<float*>(cv.take(size_t(2) * paged_attn_ctas() * (p->hq / c->g) * (c->d + 2) * 4));
+  L.parts = static_cast<float*>(cv.take(size_t(2) * paged_attn_ctas(p->hq / c->g) * (p->hq / c->g) * (c->d + 2) * 4));
   L.arrived = static_cast<unsigned int*>(cv.take(size_t(rows) * c->g * 4));
   L.bytes = cv.off;
   return L;
@@ -257,10 +263,39 @@ msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
   static msa_status_t attr = MSA_OK;
   std::call_once(once, [] { attr = set_smem(paged_attn_kernel<D, NT>, C::smem_bytes(kScanMaxBatch)); });
   if (attr != MSA_OK) return fail(attr, "paged attention: shared memory");
-  const int64_t most = int64_t(P.view.batch) * P.view.S * P.G * P.k * (P.bk / 16);   // strips
-  const int64_t grid = std::min<int64_t>(paged_attn_ctas(), (most + kPagedAttnLeast - 1) / kPagedAttnLeast);
+  const int64_t most = int64_t(P.view.batch) * P.view.S * P.G * (int64_t(P.k) << (P.bk_shift - 4));   // strips
+  const int64_t grid = std::min<int64_t>(paged_attn_ctas(P.R), (most + kPagedAttnLeast - 1) / kPagedAttnLeast);
   ProfScope ps(kPPagedAttn, st);
   return launch_step(paged_attn_kernel<D, NT>, grid, kPagedAttnWarps * 32, C::smem_bytes(P.view.batch), true, st, P);
+}
+
+// One launch for the whole decode: clusters of all (row, group)s resident at once, and an index scan that one
+// cluster does in about the time that the other kernels' launches take (1 MB of keys at capacity).
+bool small_decode(const msa_paged_cache* c, const msa_paged_decode_params* p) {
+  const int64_t clusters = int64_t(p->batch) * p->n_new * c->g;
+  const int64_t capacity = int64_t(p->max_pages) * c->page_size;
+  return clusters * kSmallCluster <= SMC * num_sms() && paged_blocks(c, p) <= kSmallBlocks &&
+         capacity * c->d_idx * 2 <= SMB;
+}
+
+template <int D, int NT, int DI>
+msa_status_t launch_paged_small(const PagedSmallParams& P, cudaStream_t st) {
+  constexpr int smem = kPagedAttnWarps * 2 * 16 * D * 2;
+  static std::once_flag once;
+  static msa_status_t attr = MSA_OK;
+  std::call_once(once, [] { attr = set_smem(paged_small_kernel<D, NT, DI>, smem); });
+  if (attr != MSA_OK) return fail(attr, "paged decode: shared memory");
+  const unsigned grid = unsigned(P.view.batch) * P.view.S * P.G * kSmallCluster;
+  ProfScope ps(kPPagedSmall, st);
+  paged_small_kernel<D, NT, DI><<<grid, kSmallThreads, smem, st>>>(P);
+  MSA_CHECK_LAUNCH();
+  return MSA_OK;
+}
+
+template <int D, int NT>
+msa_status_t dispatch_paged_small(int d_idx, const PagedSmallParams& P, cudaStream_t st) {
+  return d_idx == 128 ? launch_paged_small<D, NT, 128>(P, st) : d_idx == 64 ? launch_paged_small<D, NT, 64>(P, st)
+                                                                            : launch_paged_small<D, NT, 32>(P, st);
 }
 
 msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_params* p, const void* q, const void* q_idx,
@@ -277,8 +312,30 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
   V.shift = page_shift(c->page_size);
   V.batch = p->batch;
   V.S = p->n_new;
+  const float scale_log2 = (p->scale == 0.0f ? 1.0f / std::sqrt(float(c->d)) : p->scale) * 1.4426950408889634f;
   const int nbmax = int(paged_blocks(c, p));
   int32_t* ids = block_ids_out ? block_ids_out : L.block_ids;
+  if (small_decode(c, p)) {
+    PagedSmallParams P{};
+    P.view = V;
+    P.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
+    P.ip = static_cast<const __nv_bfloat16*>(c->k_idx);
+    P.q = static_cast<const __nv_bfloat16*>(q);
+    P.kp = static_cast<const __nv_bfloat16*>(c->k);
+    P.vp = static_cast<const __nv_bfloat16*>(c->v);
+    P.i_stride = c->k_idx_page_stride;
+    P.k_stride = c->k_page_stride;
+    P.v_stride = c->v_page_stride;
+    P.block_ids = ids;
+    P.o = static_cast<__nv_bfloat16*>(o);
+    P.G = c->g;
+    P.R = p->hq / c->g;
+    P.k = p->k;
+    P.bk_shift = page_shift(p->bk);
+    P.scale_log2 = scale_log2;
+    if (P.R <= 8) return c->d == 128 ? dispatch_paged_small<128, 1>(c->d_idx, P, st) : dispatch_paged_small<64, 1>(c->d_idx, P, st);
+    return c->d == 128 ? dispatch_paged_small<128, 2>(c->d_idx, P, st) : dispatch_paged_small<64, 2>(c->d_idx, P, st);
+  }
   msa_status_t s;
   bool scanned = false;
   if (p->k > 1 && nbmax > p->k) {   // else every visible block is taken, or the local one alone
@@ -348,8 +405,8 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
   ap.G = c->g;
   ap.R = p->hq / c->g;
   ap.k = p->k;
-  ap.bk = p->bk;
-  ap.scale_log2 = (p->scale == 0.0f ? 1.0f / std::sqrt(float(c->d)) : p->scale) * 1.4426950408889634f;
+  ap.bk_shift = page_shift(p->bk);
+  ap.scale_log2 = scale_log2;
   if (ap.R <= 8) return c->d == 128 ? launch_paged_attn<128, 1>(ap, st) : launch_paged_attn<64, 1>(ap, st);
   return c->d == 128 ? launch_paged_attn<128, 2>(ap, st) : launch_paged_attn<64, 2>(ap, st);
 }

@@ -304,11 +304,22 @@ DECODE = [
 ]
 
 
+def _wider(table, ps, di):
+    """The same table with room for 2 MB of index keys a group and sequence: calls of that capacity take
+    the kernels for long sequences."""
+    wide = torch.full((table.shape[0], max(table.shape[1], -(-(1 << 20) // (di * ps)) + 3)), -9, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lengths,S,Hq,G,d,di,k,bk,ps", DECODE)
-def test_decode_matches_fp64(cuda_ok, lengths, S, Hq, G, d, di, k, bk, ps):
+def test_decode_matches_fp64(cuda_ok, lengths, S, Hq, G, d, di, k, bk, ps, wide):
     gen = _gen(sum(lengths) + k)
     max_pages = -(-max(lengths) // ps) + 2
     cache, table, _, seq, q, qi = _filled(gen, lengths, ps, G, d, di, S, Hq, max_pages)
+    if wide:
+        table = _wider(table, ps, di)
     ids = torch.full((len(lengths), S, G, k), -9, dtype=torch.int32, device="cuda")
     o = msa.paged_decode(cache, table, seq, q, qi, k, bk=bk, block_ids=ids)
     msa.check_device_error()
@@ -317,6 +328,7 @@ def test_decode_matches_fp64(cuda_ok, lengths, S, Hq, G, d, di, k, bk, ps):
     assert torch.equal(o, again)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("shared,own,S,Hq,G,d,di,k,bk,ps", [
     (8, [700, 1, 0, 130], 1, 8, 2, 64, 32, 4, 128, 16),      # a prefix of one block
     (5, [300, 20, 900], 1, 16, 4, 128, 64, 5, 128, 16),      # shorter than a block
@@ -325,21 +337,31 @@ def test_decode_matches_fp64(cuda_ok, lengths, S, Hq, G, d, di, k, bk, ps):
     (9, [40, 1000], 4, 12, 3, 128, 32, 8, 64, 128),
     (3, [100] * 70, 2, 4, 2, 64, 64, 4, 32, 256),            # 140 rows: two row tiles
     (40, [17] * 150, 2, 1, 1, 64, 128, 8, 32, 32),           # 300 rows: three
+    (24, [300, 20, 900], 2, 16, 1, 128, 128, 5, 64, 16),     # R = 16
+    (30, [9, 8, 7, 100], 1, 10, 2, 64, 64, 13, 32, 32),      # R = 5
+    (12, [260] * 9, 4, 9, 1, 64, 32, 6, 128, 64),            # R = 9, 36 rows
     (17, [-200, -1, 0, -272, 33], 1, 8, 2, 64, 32, 4, 32, 16),   # sequences that end inside the prefix, or are empty
 ])
-def test_decode_behind_a_shared_prefix(cuda_ok, shared, own, S, Hq, G, d, di, k, bk, ps):
+def test_decode_behind_a_shared_prefix(cuda_ok, shared, own, S, Hq, G, d, di, k, bk, ps, wide):
     gen = _gen(shared * 31 + k)
     lengths = [max(0, shared * ps + n) for n in own]
     max_pages = -(-max(lengths) // ps) + 1
     cache, table, common, seq, q, qi = _filled(gen, lengths, ps, G, d, di, S, Hq, max_pages, shared=shared)
+    if wide:
+        table = _wider(table, ps, di)
     full = table.clone()
     table[:, :shared] = -1   # the prefix's columns are not read
     ids = torch.full((len(lengths), S, G, k), -9, dtype=torch.int32, device="cuda")
     o = msa.paged_decode(cache, table, seq, q, qi, k, bk=bk, prefix_pages=common, block_ids=ids)
     msa.check_device_error()
     _check_decode(cache, table, seq, q, qi, k, bk, None, o, ids, full)
-    # the same pages through the table alone
-    assert torch.equal(o, msa.paged_decode(cache, full, seq, q, qi, k, bk=bk))
+    assert torch.equal(o, msa.paged_decode(cache, table, seq, q, qi, k, bk=bk, prefix_pages=common))
+    # the same pages through the table alone: the same selection; weights are rounded to bf16 against
+    # other maxima (a slot's, not the running one), so the outputs agree with fp64 and not in every bit
+    plain_ids = torch.empty_like(ids)
+    plain = msa.paged_decode(cache, full, seq, q, qi, k, bk=bk, block_ids=plain_ids)
+    assert torch.equal(ids, plain_ids)
+    _check_decode(cache, full, seq, q, qi, k, bk, None, plain, plain_ids)
 
 
 def test_decode_scale_single_token_form_and_strided_pages(cuda_ok):
@@ -359,10 +381,13 @@ def test_decode_scale_single_token_form_and_strided_pages(cuda_ok):
     _check_decode(cache, table, seq, q, qi, k, 128, 0.5, o[:, None], ids[:, None])
 
 
-def test_decode_selects_the_lower_of_equal_blocks(cuda_ok):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_selects_the_lower_of_equal_blocks(cuda_ok, wide):
     """All index keys alike: the first k - 1 blocks and the local one; -0 and +0 are equal."""
     gen = _gen(13)
     cache, table, _, seq, q, qi = _filled(gen, [2000], 16, 2, 64, 32, 1, 4, 130, hot=False)
+    if wide:
+        table = _wider(table, 16, 32)
     cache.k_idx_pages.zero_()
     cache.k_idx_pages[::2] = -0.0
     ids = torch.empty(1, 1, 2, 5, dtype=torch.int32, device="cuda")
@@ -386,18 +411,21 @@ def test_decode_matches_the_contiguous_forward(cuda_ok):
     assert (want.float() - got.float()).abs().max() <= 2e-2
 
 
-def test_decode_reports_bad_pages_and_lengths(cuda_ok):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_reports_bad_pages_and_lengths(cuda_ok, wide):
     gen = _gen(15)
     lengths = [1000, 1000, 1000]
     cache, table, common, seq, q, qi = _filled(gen, lengths, 16, 2, 64, 32, 1, 8, 64, shared=16)
+    if wide:
+        table = _wider(table, 16, 32)
     good = msa.paged_decode(cache, table, seq, q, qi, 4, bk=32)
     msa.check_device_error()
     for what in ("page", "long", "negative", "prefix"):
         t, n, pre = table.clone(), seq.clone(), None
         if what == "page":
-            t[1, 3:60] = cache.num_pages
+            t[1, :60] = cache.num_pages
         elif what == "long":
-            n[1] = 64 * 16 + 1
+            n[1] = table.shape[1] * 16 + 1
         elif what == "negative":
             n[1] = -3
         else:
