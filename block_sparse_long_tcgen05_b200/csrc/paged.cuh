@@ -185,10 +185,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) paged_scan_kernel(const __gri
 
 // ------------------------------------------------------------------------------------
 // Top-k of every (row, group): the local block and the k - 1 best earlier ones, equal scores
-// the lower block first; ascending ids, padded with -1. One warp per (row, group), 1024 keys at
-// a time in its registers (lane l: keys l, l + 32, ...); k - 1 times the best one is found by a
-// warp-wide max of the keys and a min of the ids among equals, and taken out. The chosen ones of
-// earlier chunks are carried as one more candidate a lane. Latency-bound.
+// the lower block first; ascending ids, padded with -1. One warp per (row, group). Latency-bound.
 // ------------------------------------------------------------------------------------
 struct PagedTopkParams {
   PageView view;
@@ -200,33 +197,90 @@ struct PagedTopkParams {
 };
 
 // The k - 1 best of the keys src[0 .. n), n >= k - 1, of one warp: lane r < k - 1 returns the r-th
-// best one's id, and in `place` its place among them in ascending order of ids.
-__device__ __forceinline__ int topk_warp(const uint32_t* src, int n, int k, int lane, int& place) {
+// best one's id, and in `place` its place among them in ascending order of ids. scratch: 96 entries of
+// the warp's own in shared memory.
+//
+// 32 NK keys at a time (lane l: keys l, l + 32, ...), the best ones of earlier chunks carried along. The
+// (k - 1)-th best of the lanes' maxima is a bound that at least k - 1 keys reach; the few keys that do
+// are put side by side and each counts those before it: 3 us less than what follows, for k = 16 of 1024.
+// Where more than 64 reach it (many equal scores), or few are wanted, the best one is taken out k - 1
+// times instead, by a warp-wide max of the keys and a min of the ids among equals.
+template <int NK>
+__device__ __forceinline__ int topk_warp_of(const uint32_t* src, int n, int k, int lane, uint2* scratch, int& place) {
   uint32_t carried = 0u, carried_id = 0xffffffffu;   // lane r: the r-th best so far (key 0: none)
-  for (int c0 = 0; k > 1 && c0 < n; c0 += 1024) {
-    uint32_t key[32];
+  for (int c0 = 0; k > 1 && c0 < n; c0 += 32 * NK) {
+    uint32_t key[NK];
+    uint32_t best = carried;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) key[j] = c0 + j * 32 + lane < n ? src[c0 + j * 32 + lane] : 0u;
+    for (int j = 0; j < NK; ++j) {
+      const int i = c0 + j * 32 + lane;
+      key[j] = i < n ? src[i] : 0u;
+      best = max(best, key[j]);
+    }
     uint32_t next = 0u, next_id = 0xffffffffu;
-    uint32_t best = 0u;
-    int at = -1;
-    for (int r = 0; r + 1 < k; ++r) {
-      best = carried;
-      at = -1;
+    uint32_t bound = 0u;
+    int count = 0, to = 0, total = 65;
+    if (k > 6) {
+      int before = 0;
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (key[j] > best) { best = key[j]; at = j; }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      if (top == 0u) break;
-      const uint32_t id = at < 0 ? carried_id : static_cast<uint32_t>(c0 + at * 32 + lane);
-      const uint32_t win = __reduce_min_sync(0xffffffffu, best == top ? id : 0xffffffffu);
-      if (best == top && id == win) {
-        if (at < 0) carried = 0u;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == at) key[j] = 0u;
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t other = __shfl_sync(0xffffffffu, best, j);
+        before += other > best || (other == best && j < lane);
       }
-      if (lane == r) { next = top; next_id = win; }
+      bound = __shfl_sync(0xffffffffu, best, __ffs(__ballot_sync(0xffffffffu, before == k - 2)) - 1);
+      count = carried >= bound && carried != 0u;
+#pragma unroll
+      for (int j = 0; j < NK; ++j) count += key[j] >= bound && key[j] != 0u;
+      to = count;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, to, o);
+        if (lane >= o) to += y;
+      }
+      total = __shfl_sync(0xffffffffu, to, 31);
+    }
+    if (total <= 64) {
+      to -= count;
+      if (carried >= bound && carried != 0u) scratch[to++] = make_uint2(carried, carried_id);
+#pragma unroll
+      for (int j = 0; j < NK; ++j)
+        if (key[j] >= bound && key[j] != 0u) scratch[to++] = make_uint2(key[j], static_cast<uint32_t>(c0 + j * 32 + lane));
+      __syncwarp();
+      const uint2 a = lane < total ? scratch[lane] : make_uint2(0u, 0xffffffffu);
+      const uint2 b = lane + 32 < total ? scratch[lane + 32] : make_uint2(0u, 0xffffffffu);
+      int ra = 0, rb = 0;   // how many come before
+      for (int j = 0; j < total; ++j) {
+        const uint2 x = scratch[j];
+        ra += x.x > a.x || (x.x == a.x && x.y < a.y);
+        rb += x.x > b.x || (x.x == b.x && x.y < b.y);
+      }
+      if (lane < total && ra < k - 1) scratch[64 + ra] = a;
+      if (lane + 32 < total && rb < k - 1) scratch[64 + rb] = b;
+      __syncwarp();
+      if (lane < k - 1 && lane < total) {
+        next = scratch[64 + lane].x;
+        next_id = scratch[64 + lane].y;
+      }
+      __syncwarp();   // the scratch is written again
+    } else {
+      for (int r = 0; r + 1 < k; ++r) {
+        best = carried;
+        int at = -1;
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+          if (key[j] > best) { best = key[j]; at = j; }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top == 0u) break;
+        const uint32_t id = at < 0 ? carried_id : static_cast<uint32_t>(c0 + at * 32 + lane);
+        const uint32_t win = __reduce_min_sync(0xffffffffu, best == top ? id : 0xffffffffu);
+        if (best == top && id == win) {
+          if (at < 0) carried = 0u;
+#pragma unroll
+          for (int j = 0; j < NK; ++j)
+            if (j == at) key[j] = 0u;
+        }
+        if (lane == r) { next = top; next_id = win; }
+      }
     }
     carried = next;
     carried_id = next_id;
@@ -237,7 +291,12 @@ __device__ __forceinline__ int topk_warp(const uint32_t* src, int n, int k, int 
   return static_cast<int>(carried_id);
 }
 
+__device__ __forceinline__ int topk_warp(const uint32_t* src, int n, int k, int lane, uint2* scratch, int& place) {
+  return n <= 128 ? topk_warp_of<4>(src, n, k, lane, scratch, place) : topk_warp_of<32>(src, n, k, lane, scratch, place);
+}
+
 __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__ PagedTopkParams P) {
+  __shared__ uint2 scratch[4][96];
   const PageView& V = P.view;
   const int64_t rg = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -259,7 +318,7 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
   grid_wait();
   const uint32_t* src = P.maxima + rg * P.nbmax;
   int place;
-  const int id = topk_warp(src, bl, P.k, lane, place);
+  const int id = topk_warp(src, bl, P.k, lane, scratch[threadIdx.x >> 5], place);
   if (lane + 1 < P.k) out[place] = id;
   if (lane == 0) out[P.k - 1] = bl;
 }

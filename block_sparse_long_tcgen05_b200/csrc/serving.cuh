@@ -1,9 +1,3 @@
-#ifndef SMC
-#define SMC 2
-#endif
-#ifndef SMB
-#define SMB (1<<20)
-#endif
 // Host side of the serving entry points (rotary positions, paged append, paged decode): their
 // argument checks, workspace layout and launches. Included by msa_api.cu after its helpers.
 #pragma once
@@ -269,33 +263,43 @@ msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
   return launch_step(paged_attn_kernel<D, NT>, grid, kPagedAttnWarps * 32, C::smem_bytes(P.view.batch), true, st, P);
 }
 
-// One launch for the whole decode: clusters of all (row, group)s resident at once, and an index scan that one
-// cluster does in about the time that the other kernels' launches take (1 MB of keys at capacity).
-bool small_decode(const msa_paged_cache* c, const msa_paged_decode_params* p) {
-  const int64_t clusters = int64_t(p->batch) * p->n_new * c->g;
-  const int64_t capacity = int64_t(p->max_pages) * c->page_size;
-  return clusters * kSmallCluster <= SMC * num_sms() && paged_blocks(c, p) <= kSmallBlocks &&
-         capacity * c->d_idx * 2 <= SMB;
-}
-
+// One launch for the whole decode. Wanted where the clusters of all (row, group)s are resident at once (they
+// gain 30 to 45% there; at twice as many the three kernels are as fast, at four times faster) and a cluster
+// scans the longest sequence in about the time that two more launches take: 16384 tokens (8 groups of 128
+// index elements: 28 us against 30; at 30000 tokens 51 against 34), 256 blocks (500 blocks of 32 tokens:
+// 23 against 17). `done`: whether it was launched.
 template <int D, int NT, int DI>
-msa_status_t launch_paged_small(const PagedSmallParams& P, cudaStream_t st) {
+msa_status_t try_paged_small(const PagedSmallParams& P, bool& done, cudaStream_t st) {
   constexpr int smem = kPagedAttnWarps * 2 * 16 * D * 2;
   static std::once_flag once;
-  static msa_status_t attr = MSA_OK;
-  std::call_once(once, [] { attr = set_smem(paged_small_kernel<D, NT, DI>, smem); });
-  if (attr != MSA_OK) return fail(attr, "paged decode: shared memory");
-  const unsigned grid = unsigned(P.view.batch) * P.view.S * P.G * kSmallCluster;
+  static int resident = 0;   // clusters
+  std::call_once(once, [] {
+    if (set_smem(paged_small_kernel<D, NT, DI>, smem) != MSA_OK) return;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSmallCluster);
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSmallCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&resident, paged_small_kernel<D, NT, DI>, &cfg) != cudaSuccess) resident = 0;
+  });
+  const int64_t clusters = int64_t(P.view.batch) * P.view.S * P.G;
+  done = clusters <= resident;
+  if (!done) return MSA_OK;
   ProfScope ps(kPPagedSmall, st);
-  paged_small_kernel<D, NT, DI><<<grid, kSmallThreads, smem, st>>>(P);
+  paged_small_kernel<D, NT, DI><<<unsigned(clusters * kSmallCluster), kSmallThreads, smem, st>>>(P);
   MSA_CHECK_LAUNCH();
   return MSA_OK;
 }
 
 template <int D, int NT>
-msa_status_t dispatch_paged_small(int d_idx, const PagedSmallParams& P, cudaStream_t st) {
-  return d_idx == 128 ? launch_paged_small<D, NT, 128>(P, st) : d_idx == 64 ? launch_paged_small<D, NT, 64>(P, st)
-                                                                            : launch_paged_small<D, NT, 32>(P, st);
+msa_status_t try_paged_small(int d_idx, const PagedSmallParams& P, bool& done, cudaStream_t st) {
+  return d_idx == 128 ? try_paged_small<D, NT, 128>(P, done, st) : d_idx == 64 ? try_paged_small<D, NT, 64>(P, done, st)
+                                                                             : try_paged_small<D, NT, 32>(P, done, st);
 }
 
 msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_params* p, const void* q, const void* q_idx,
@@ -315,7 +319,8 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
   const float scale_log2 = (p->scale == 0.0f ? 1.0f / std::sqrt(float(c->d)) : p->scale) * 1.4426950408889634f;
   const int nbmax = int(paged_blocks(c, p));
   int32_t* ids = block_ids_out ? block_ids_out : L.block_ids;
-  if (small_decode(c, p)) {
+  msa_status_t s;
+  if (int64_t(p->max_pages) * c->page_size <= 16384 && nbmax <= kSmallBlocks) {
     PagedSmallParams P{};
     P.view = V;
     P.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
@@ -333,10 +338,11 @@ msa_status_t run_paged_decode(const msa_paged_cache* c, const msa_paged_decode_p
     P.k = p->k;
     P.bk_shift = page_shift(p->bk);
     P.scale_log2 = scale_log2;
-    if (P.R <= 8) return c->d == 128 ? dispatch_paged_small<128, 1>(c->d_idx, P, st) : dispatch_paged_small<64, 1>(c->d_idx, P, st);
-    return c->d == 128 ? dispatch_paged_small<128, 2>(c->d_idx, P, st) : dispatch_paged_small<64, 2>(c->d_idx, P, st);
+    bool done = false;
+    if (P.R <= 8) s = c->d == 128 ? try_paged_small<128, 1>(c->d_idx, P, done, st) : try_paged_small<64, 1>(c->d_idx, P, done, st);
+    else s = c->d == 128 ? try_paged_small<128, 2>(c->d_idx, P, done, st) : try_paged_small<64, 2>(c->d_idx, P, done, st);
+    if (done || s != MSA_OK) return s;
   }
-  msa_status_t s;
   bool scanned = false;
   if (p->k > 1 && nbmax > p->k) {   // else every visible block is taken, or the local one alone
     PagedScanParams sp{};

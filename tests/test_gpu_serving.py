@@ -304,10 +304,9 @@ DECODE = [
 ]
 
 
-def _wider(table, ps, di):
-    """The same table with room for 2 MB of index keys a group and sequence: calls of that capacity take
-    the kernels for long sequences."""
-    wide = torch.full((table.shape[0], max(table.shape[1], -(-(1 << 20) // (di * ps)) + 3)), -9, dtype=torch.int32, device="cuda")
+def _wider(table, ps):
+    """The same table with room for 20000 tokens: calls of that capacity take the kernels for long sequences."""
+    wide = torch.full((table.shape[0], max(table.shape[1], 20000 // ps + 1)), -9, dtype=torch.int32, device="cuda")
     wide[:, :table.shape[1]] = table
     return wide
 
@@ -319,7 +318,7 @@ def test_decode_matches_fp64(cuda_ok, lengths, S, Hq, G, d, di, k, bk, ps, wide)
     max_pages = -(-max(lengths) // ps) + 2
     cache, table, _, seq, q, qi = _filled(gen, lengths, ps, G, d, di, S, Hq, max_pages)
     if wide:
-        table = _wider(table, ps, di)
+        table = _wider(table, ps)
     ids = torch.full((len(lengths), S, G, k), -9, dtype=torch.int32, device="cuda")
     o = msa.paged_decode(cache, table, seq, q, qi, k, bk=bk, block_ids=ids)
     msa.check_device_error()
@@ -348,7 +347,7 @@ def test_decode_behind_a_shared_prefix(cuda_ok, shared, own, S, Hq, G, d, di, k,
     max_pages = -(-max(lengths) // ps) + 1
     cache, table, common, seq, q, qi = _filled(gen, lengths, ps, G, d, di, S, Hq, max_pages, shared=shared)
     if wide:
-        table = _wider(table, ps, di)
+        table = _wider(table, ps)
     full = table.clone()
     table[:, :shared] = -1   # the prefix's columns are not read
     ids = torch.full((len(lengths), S, G, k), -9, dtype=torch.int32, device="cuda")
@@ -387,7 +386,7 @@ def test_decode_selects_the_lower_of_equal_blocks(cuda_ok, wide):
     gen = _gen(13)
     cache, table, _, seq, q, qi = _filled(gen, [2000], 16, 2, 64, 32, 1, 4, 130, hot=False)
     if wide:
-        table = _wider(table, 16, 32)
+        table = _wider(table, 16)
     cache.k_idx_pages.zero_()
     cache.k_idx_pages[::2] = -0.0
     ids = torch.empty(1, 1, 2, 5, dtype=torch.int32, device="cuda")
@@ -417,7 +416,7 @@ def test_decode_reports_bad_pages_and_lengths(cuda_ok, wide):
     lengths = [1000, 1000, 1000]
     cache, table, common, seq, q, qi = _filled(gen, lengths, 16, 2, 64, 32, 1, 8, 64, shared=16)
     if wide:
-        table = _wider(table, 16, 32)
+        table = _wider(table, 16)
     good = msa.paged_decode(cache, table, seq, q, qi, 4, bk=32)
     msa.check_device_error()
     for what in ("page", "long", "negative", "prefix"):
