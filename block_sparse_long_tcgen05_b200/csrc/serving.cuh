@@ -163,6 +163,18 @@ msa_status_t launch_step(void (*kernel)(Params...), int64_t grid, int threads, i
   return MSA_OK;
 }
 
+// Shared-memory limit of a kernel, set once on each device that it is launched on.
+template <typename K>
+msa_status_t smem_limit(std::atomic<uint64_t>& done, K kernel, int bytes) {
+  int dev = 0;
+  MSA_CHECK_CUDA(cudaGetDevice(&dev));
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return MSA_OK;
+  const msa_status_t s = set_smem(kernel, bytes);
+  if (s == MSA_OK) done.fetch_or(bit, std::memory_order_release);
+  return s;
+}
+
 struct PagedLayout {
   uint32_t* maxima = nullptr;
   int32_t* block_ids = nullptr;
@@ -223,10 +235,9 @@ msa_status_t launch_paged_scan(const PagedScanParams& P, bool after, cudaStream_
 template <int DI, int RT>
 msa_status_t launch_prefix_scan(const CUtensorMap& tq, const CUtensorMap& tk, PrefixScanParams P, cudaStream_t st) {
   using C = PrefixCfg<DI, RT>;
-  static std::once_flag once;
-  static msa_status_t attr = MSA_OK;
-  std::call_once(once, [] { attr = set_smem(prefix_scan_kernel<DI, RT>, C::kSmemBytes); });
-  if (attr != MSA_OK) return fail(attr, "prefix scan: shared memory");
+  static std::atomic<uint64_t> limit{0};
+  msa_status_t s;
+  if ((s = smem_limit(limit, prefix_scan_kernel<DI, RT>, C::kSmemBytes)) != MSA_OK) return s;
   const int sms = num_sms();
   P.pairs = (P.rows + RT * 128 - 1) / (RT * 128) * P.G;
   P.workers = std::max(1, std::min(sms / P.pairs, P.tiles));
@@ -253,10 +264,9 @@ msa_status_t run_prefix_scan(const msa_paged_cache* c, const void* q_idx, const 
 template <int D, int NT>
 msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
   using C = PagedAttnCfg<D>;
-  static std::once_flag once;
-  static msa_status_t attr = MSA_OK;
-  std::call_once(once, [] { attr = set_smem(paged_attn_kernel<D, NT>, C::smem_bytes(kScanMaxBatch)); });
-  if (attr != MSA_OK) return fail(attr, "paged attention: shared memory");
+  static std::atomic<uint64_t> limit{0};
+  msa_status_t s;
+  if ((s = smem_limit(limit, paged_attn_kernel<D, NT>, C::smem_bytes(kScanMaxBatch))) != MSA_OK) return s;
   const int64_t most = int64_t(P.view.batch) * P.view.S * P.G * (int64_t(P.k) << (P.bk_shift - 4));   // strips
   const int64_t grid = std::min<int64_t>(paged_attn_ctas(P.R), (most + kPagedAttnLeast - 1) / kPagedAttnLeast);
   ProfScope ps(kPPagedAttn, st);
@@ -271,10 +281,12 @@ msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
 template <int D, int NT, int DI>
 msa_status_t try_paged_small(const PagedSmallParams& P, bool& done, cudaStream_t st) {
   constexpr int smem = kPagedAttnWarps * 2 * 16 * D * 2;
+  static std::atomic<uint64_t> limit{0};
+  msa_status_t s;
+  if ((s = smem_limit(limit, paged_small_kernel<D, NT, DI>, smem)) != MSA_OK) return s;
   static std::once_flag once;
   static int resident = 0;   // clusters
   std::call_once(once, [] {
-    if (set_smem(paged_small_kernel<D, NT, DI>, smem) != MSA_OK) return;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kSmallCluster);
     cfg.blockDim = dim3(kSmallThreads);

@@ -368,6 +368,8 @@ _PACK_ROPE = struct.Struct("@iiiifiPP").pack
 _PACK_APPEND = struct.Struct("@iiiiiifqPPPPP").pack
 _PACK_DECODE = struct.Struct("@iiiiiiifqPPP").pack
 _fast = None
+_current_device = getattr(torch._C, "_cuda_getDevice", None)          # absent in builds without CUDA
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _serving():
@@ -393,7 +395,7 @@ def _heads(x: torch.Tensor, name: str, n: int, index: int, dtype, y: torch.Tenso
     shape, sx = x.shape, x.stride()
     if len(shape) != 3 or shape[0] != n:
         raise ValueError(f"{name} must be [{n}, heads, dim]")
-    if x.dtype != dtype or x.get_device() != index:
+    if x.dtype is not dtype or x.get_device() != index:
         raise ValueError(f"{name} must be {dtype} on device {index}")
     if sx[2] != 1 and shape[2] != 1:
         raise ValueError(f"{name}: the elements of a head must lie side by side")
@@ -403,31 +405,32 @@ def _heads(x: torch.Tensor, name: str, n: int, index: int, dtype, y: torch.Tenso
     if y is None:
         return _PACK_TENSOR(x.data_ptr(), 0, sx[0], sx[1], 0, 0, shape[1], shape[2])
     sy = y.stride()
-    if y.shape != shape or y.dtype != y_dtype or y.get_device() != index or (sy[2] != 1 and shape[2] != 1):
+    if y.dtype is not y_dtype or y.shape != shape or y.get_device() != index or (sy[2] != 1 and shape[2] != 1):
         raise ValueError(f"{name}: its result must be {y_dtype} {list(shape)} on device {index}, heads' elements side by side")
     return _PACK_TENSOR(x.data_ptr(), y.data_ptr(), sx[0], sx[1], sy[0], sy[1], shape[1], shape[2])
 
 
 def _small(t: torch.Tensor, name: str, index: int, dtype, shape) -> int:
     """Address of a contiguous tensor of known shape, type and device."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} on device {index}")
     return t.data_ptr()
 
 
 def _freqs(t: torch.Tensor, name: str, index: int) -> tuple[int, int]:
-    if t.dtype != torch.float64 or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype is not torch.float64 or len(shape) != 1 or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float64 [rot / 2] on device {index}")
-    return t.data_ptr(), 2 * t.shape[0]
+    return t.data_ptr(), 2 * shape[0]
 
 
 def _launch(index: int, fn, *args) -> None:
     """fn(*args, stream) on the tensors' device, whichever device is the current one."""
-    if index == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == _current_device():
+        st = fn(*args, _current_stream(index))
     else:
         with torch.cuda.device(index):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            st = fn(*args, _current_stream(index))
     if st != MSA_OK:
         _check(st)
 

@@ -394,6 +394,55 @@ def test_decode_selects_the_lower_of_equal_blocks(cuda_ok, wide):
     assert ids.flatten(0, 2).tolist() == [[0, 1, 2, 3, 62]] * 2
 
 
+def test_decode_of_thousands_of_short_sequences(cuda_ok):
+    gen = _gen(19)
+    lengths = [int(x) for x in torch.randint(0, 300, (2100,), generator=torch.Generator().manual_seed(3))]
+    cache, table, _, seq, q, qi = _filled(gen, lengths, 64, 1, 64, 32, 1, 2, 5)
+    ids = torch.empty(2100, 1, 1, 4, dtype=torch.int32, device="cuda")
+    o = msa.paged_decode(cache, table, seq, q, qi, 4, bk=32, block_ids=ids)
+    msa.check_device_error()
+    _check_decode(cache, table, seq, q, qi, 4, 32, None, o, ids)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_pages_beyond_2_31_elements(cuda_ok, wide):
+    """A pool of 2^31 elements and more: append to and decode from its last pages gives what a small pool
+    gives, bit for bit."""
+    gen = _gen(20)
+    ps, G, d, di, k = 128, 8, 128, 128, 4
+    pages = (1 << 31) // (ps * G * d) + 16
+    far, near = (msa.PagedCache(*(torch.empty(n, ps, G, w, dtype=torch.bfloat16, device="cuda") for w in (d, d, di)))
+                 for n in (pages, 16))
+    lengths = [900, 300, 500]
+    B, seq = 3, torch.tensor([900, 300, 500], dtype=torch.int32, device="cuda")
+    table, common = _deal(gen, lengths, ps, 9, 16, shared=1)
+    if wide:
+        table = _wider(table, ps)
+    cu = torch.tensor([0, 900, 1200, 1700], dtype=torch.int32, device="cuda")
+    f, s = msa.rope_frequencies(128)
+    new = [_randn(gen, 1700, G, d), _randn(gen, 1700, G, d), _ints(gen, 1700, G, di)]
+    q, qi = _randn(gen, B, 16, d), _ints(gen, B, G, di)
+    out = []
+    for cache, shift in ((far, pages - 16), (near, 0)):
+        at = torch.where(table >= 0, table + shift, table).to(torch.int32)
+        # the first page is every sequence's: the last writer's keys would depend on the order, so one writes
+        msa.paged_append(cache, at[:1].contiguous(), seq[:1], *(x[:900] for x in new), freqs=f, rotate_index=False)
+        for b in (1, 2):
+            at_b = at[b:b + 1].clone()
+            lo = int(cu[b])
+            at_b[0, 0] = int(at_b[0, 1])   # its first page's tokens go where its second's come after them
+            msa.paged_append(cache, at_b, torch.tensor([128], dtype=torch.int32, device="cuda"), *(x[lo:lo + 128] for x in new),
+                             freqs=f, rotate_index=False)
+            msa.paged_append(cache, at[b:b + 1].contiguous(), seq[b:b + 1], *(x[lo + 128:lo + lengths[b]] for x in new), freqs=f,
+                             rotate_index=False)
+        ids = torch.empty(B, G, k, dtype=torch.int32, device="cuda")
+        o = msa.paged_decode(cache, at, seq, q, qi, k, prefix_pages=(common + shift).to(torch.int32), block_ids=ids)
+        msa.check_device_error()
+        out.append((o, ids))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert out[0][0].isfinite().all()
+
+
 def test_decode_matches_the_contiguous_forward(cuda_ok):
     """The same cache through msa.decode: equal selections, outputs within both's tolerance."""
     gen = _gen(14)
@@ -449,7 +498,8 @@ def _fresh_step(gen, B, G, Hq, d, di):
     return x
 
 
-def test_prompt_and_steps_as_a_server_makes_them(cuda_ok):
+@pytest.mark.parametrize("wide", [False, True])
+def test_prompt_and_steps_as_a_server_makes_them(cuda_ok, wide):
     """Prompts appended in ragged chunks behind a shared prefix, then steps of one token: rotation,
     append and decode, each step checked against fp64 on the cache; then a captured step replayed on
     new tokens and lengths gives what the eager one does, bit for bit."""
@@ -461,6 +511,8 @@ def test_prompt_and_steps_as_a_server_makes_them(cuda_ok):
     order = torch.randperm(cache.num_pages, generator=gen, device="cuda").to(torch.int32)
     common = order[:shared].contiguous()
     table = torch.cat([common.expand(B, shared), order[shared:shared + B * (max_pages - shared)].view(B, -1)], 1).contiguous()
+    if wide:
+        table = _wider(table, ps)
     # the prefix, once, as a sequence of its own
     P = shared * ps
     x = _fresh_step(gen, P, G, Hq, d, di)
@@ -476,7 +528,7 @@ def test_prompt_and_steps_as_a_server_makes_them(cuda_ok):
            "q_idx": torch.empty(B, G, di, dtype=torch.bfloat16, device="cuda"),
            "o": torch.empty(B, Hq, d, dtype=torch.bfloat16, device="cuda"),
            "ids": torch.empty(B, G, k, dtype=torch.int32, device="cuda")}
-    ws = torch.empty(msa.paged_decode_workspace(cache, B, max_pages, Hq, k), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(msa.paged_decode_workspace(cache, B, table.shape[1], Hq, k), dtype=torch.uint8, device="cuda")
     x = _fresh_step(gen, B, G, Hq, d, di)
     for _ in range(3):
         seq += 1
@@ -514,11 +566,14 @@ def test_prompt_and_steps_as_a_server_makes_them(cuda_ok):
                       out["ids"][:, None])
 
 
-def test_calls_on_two_streams(cuda_ok):
+@pytest.mark.parametrize("wide", [False, True])
+def test_calls_on_two_streams(cuda_ok, wide):
     """Two decodes at once, each with a workspace of its own, give what they give alone."""
     gen = _gen(17)
-    a = _filled(gen, [3000, 500], 64, 2, 128, 64, 1, 16, 50)
-    b = _filled(gen, [100, 2900, 1], 16, 2, 64, 32, 2, 8, 200, shared=10)
+    a = list(_filled(gen, [3000, 500], 64, 2, 128, 64, 1, 16, 50))
+    b = list(_filled(gen, [100, 2900, 1], 16, 2, 64, 32, 2, 8, 200, shared=10))
+    if wide:
+        a[1], b[1] = _wider(a[1], 64), _wider(b[1], 16)
     run = lambda c, pre: msa.paged_decode(c[0], c[1], c[3], c[4], c[5], 8, prefix_pages=c[2] if pre else None)  # noqa: E731
     want = run(a, False), run(b, False)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
