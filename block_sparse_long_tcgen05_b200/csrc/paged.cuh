@@ -285,9 +285,13 @@ __device__ __forceinline__ int topk_warp_of(const uint32_t* src, int n, int k, i
     carried = next;
     carried_id = next_id;
   }
-  // ascending: an id's place is the number of smaller ones
+  // ascending: an id's place is the number of smaller ones (ids that were not found, behind a scan that
+  // gave up, are -1 and take the last places)
   place = 0;
-  for (int r = 0; r + 1 < k; ++r) place += __shfl_sync(0xffffffffu, carried_id, r) < carried_id;
+  for (int r = 0; r + 1 < k; ++r) {
+    const uint32_t other = __shfl_sync(0xffffffffu, carried_id, r);
+    place += other < carried_id || (other == carried_id && r < lane);
+  }
   return static_cast<int>(carried_id);
 }
 
@@ -642,7 +646,7 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) page
       const int blk = __ldg(P.block_ids + ((static_cast<int64_t>(x.b) * V.S + x.s) * P.G + x.g) * P.k + (x.at >> per_shift));
       const int t0 = (blk << P.bk_shift) + ((x.at & ((1 << per_shift) - 1)) << 4);
       int page = -1;
-      if (blk >= 0 && t0 <= x.pos) page = static_cast<int>(page_of(V, x.b, t0, kKidPagedAttn));
+      if (blk >= 0 && blk <= x.pos >> P.bk_shift && t0 <= x.pos) page = static_cast<int>(page_of(V, x.b, t0, kKidPagedAttn));
       const int seen = page >= 0 ? min(16, x.pos - t0 + 1) : 0;
       table[i] = make_int2(page, (t0 & ((1 << V.shift) - 1)) << 16 | x.g << 8 | seen);
     }

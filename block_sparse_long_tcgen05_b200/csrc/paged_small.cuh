@@ -147,8 +147,9 @@ paged_small_kernel(const __grid_constant__ PagedSmallParams P) {
   auto place_of = [&](int i) {
     Place x{-1, 0, 0};
     if (i < strips) {
-      const int t0 = (ids[i >> per_shift] << P.bk_shift) + ((i & ((1 << per_shift) - 1)) << 4);
-      if (t0 <= pos) x.page = page_of(V, b, t0, kKidPagedSmall);
+      const int blk = ids[i >> per_shift];
+      const int t0 = (blk << P.bk_shift) + ((i & ((1 << per_shift) - 1)) << 4);
+      if (blk >= 0 && t0 <= pos) x.page = page_of(V, b, t0, kKidPagedSmall);
       x.row = t0 & mask;
       x.seen = x.page >= 0 ? min(16, pos - t0 + 1) : 0;
     }

@@ -339,6 +339,12 @@ def test_decode_matches_fp64(cuda_ok, lengths, S, Hq, G, d, di, k, bk, ps, wide)
     (24, [300, 20, 900], 2, 16, 1, 128, 128, 5, 64, 16),     # R = 16
     (30, [9, 8, 7, 100], 1, 10, 2, 64, 64, 13, 32, 32),      # R = 5
     (12, [260] * 9, 4, 9, 1, 64, 32, 6, 128, 64),            # R = 9, 36 rows
+    # prefixes worth a scan of their own (16 MB of keys spared)
+    (21, [1, 64, 511, 4] * 10, 1, 4, 2, 64, 128, 5, 128, 64),        # ends inside a block; one row tile
+    (5, [100, 0, -1270] * 24, 2, 4, 2, 64, 64, 4, 32, 256),          # 144 rows: two row tiles; sequences that end inside
+    (70, [33, 1, 200] * 30, 1, 12, 3, 128, 32, 8, 32, 16),           # 35 blocks: the last tile of 128 tokens is not full
+    (2, [5, 900] * 15, 1, 8, 4, 128, 128, 3, 128, 1024),             # pages of more than a tile
+    (3, [9, 40] * 300, 1, 64, 64, 64, 32, 2, 32, 32),                # 192 pairs of row tiles and groups: more than SMs
     (17, [-200, -1, 0, -272, 33], 1, 8, 2, 64, 32, 4, 32, 16),   # sequences that end inside the prefix, or are empty
 ])
 def test_decode_behind_a_shared_prefix(cuda_ok, shared, own, S, Hq, G, d, di, k, bk, ps, wide):
@@ -483,6 +489,40 @@ def test_decode_reports_bad_pages_and_lengths(cuda_ok, wide):
         assert msa.msa_get_device_error() == 6, what
         if what != "prefix":
             assert torch.equal(o[0], good[0]) and torch.equal(o[2], good[2])
+
+
+def test_decode_reports_bad_pages_of_a_scanned_prefix(cuda_ok):
+    gen = _gen(21)
+    lengths = [2100] * 30
+    cache, table, common, seq, q, qi = _filled(gen, lengths, 64, 4, 64, 128, 1, 8, 34, shared=32)
+    table = _wider(table, 64)
+    good = msa.paged_decode(cache, table, seq, q, qi, 4, prefix_pages=common)
+    msa.check_device_error()
+    for bad in (-1, cache.num_pages, 2 ** 31 - 1):
+        pre = common.clone()
+        pre[7] = bad
+        msa.paged_decode(cache, table, seq, q, qi, 4, prefix_pages=pre)
+        assert msa.msa_get_device_error() == 6
+    assert torch.equal(good, msa.paged_decode(cache, table, seq, q, qi, 4, prefix_pages=common))
+    msa.check_device_error()
+
+
+def test_prefix_scan_waits_end(cuda_ok):
+    """The prefix scan's gating waits are bounded: with a limit that every wait exceeds, the call ends
+    with a timeout status and the next one, at the default, is right again."""
+    gen = _gen(22)
+    cache, table, common, seq, q, qi = _filled(gen, [2100] * 30, 64, 4, 64, 128, 1, 8, 34, shared=32)
+    table = _wider(table, 64)
+    good = msa.paged_decode(cache, table, seq, q, qi, 4, prefix_pages=common)
+    msa.check_device_error()
+    msa.set_wait_limit_ns(1)
+    try:
+        msa.paged_decode(cache, table, seq, q, qi, 4, prefix_pages=common)
+        assert msa.msa_get_device_error() == 5
+    finally:
+        msa.set_wait_limit_ns(0)
+    assert torch.equal(good, msa.paged_decode(cache, table, seq, q, qi, 4, prefix_pages=common))
+    msa.check_device_error()
 
 
 # ------------------------------------------------------------------------------------ together
