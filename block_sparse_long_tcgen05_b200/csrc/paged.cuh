@@ -375,7 +375,7 @@ struct PagedAttnCfg {
   static_assert(2 * kEight * 4 >= 18 * 16 * 8, "the shares fit the join's memory");
   static constexpr int kJoinOff = kPagedAttnWarps * kPagedAttnRing * kStrip * 2;
   static constexpr int kTableOff = kJoinOff + 2 * kEight * 4;
-  static constexpr int kEndsOff = kTableOff + kPagedAttnTable * 8;
+  static constexpr int kEndsOff = kTableOff + kPagedAttnTable * 16;
   static constexpr int smem_bytes(int batch) { return kEndsOff + batch * 4; }
 };
 
@@ -397,6 +397,22 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Starts the copies of a strip's 16 rows of values (rows from `seen` on: zeros, whatever lies there) to
+// shared address dst, 16-byte pieces c of row r at c ^ (r % 8), so that ldmatrix rows hit distinct banks.
+template <int D>
+__device__ __forceinline__ void fetch_values(uint32_t dst, const __nv_bfloat16* src, int64_t row, int seen, int lane) {
+  constexpr int C = D / 8, STEP = 32 / C;   // pieces of a row, rows of a warp's access
+  const int r0 = lane / C, c = lane % C;
+  const __nv_bfloat16* s = src + r0 * row + c * 8;
+  const uint32_t d = dst + r0 * D * 2, x = (c ^ r0) << 4;
+#pragma unroll
+  for (int i = 0; i < 16 / STEP; ++i) {   // r0 < STEP: (r0 + i STEP) % 8 is r0 | (i STEP) % 8
+    const uint32_t to = d + i * STEP * D * 2 + (x ^ (((i * STEP) & 7) << 4));
+    const int bytes = r0 + i * STEP < seen ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(s + i * STEP * row), "r"(bytes) : "memory");
+  }
 }
 
 // S^T of a strip: keys kx, ky as they lie (rows gq and gq + 8), queries qf in the same order of elements;
@@ -564,7 +580,7 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) page
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
   float* join = reinterpret_cast<float*>(psm + C::kJoinOff);
-  int2* table = reinterpret_cast<int2*>(psm + C::kTableOff);   // page; row in the page, group, tokens seen
+  longlong2* table = reinterpret_cast<longlong2*>(psm + C::kTableOff);   // first key element * 32 + tokens seen, first value element
   int* ends = reinterpret_cast<int*>(psm + C::kEndsOff);
   // running total of the sequences' strips
   int total = 0;
@@ -602,29 +618,21 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) page
   // starts the copies of the values of entry i of the table
   auto fetch_v = [&](int i, int count, int stage) {
     if (i < count) {
-      const int2 at = table[i];
-      const int seen = at.y & 31;
-      if (seen > 0) {
-        const __nv_bfloat16* vs = P.vp + at.x * P.v_stride + static_cast<int64_t>(at.y >> 16) * row + ((at.y >> 8) & 255) * D;
-        __nv_bfloat16* vd = ring + stage * C::kStrip;
-#pragma unroll
-        for (int e = lane; e < 16 * (D / 8); e += 32) {
-          const int r = e / (D / 8), c = e % (D / 8);
-          const bool ok = r < seen;   // rows behind the position read as zeros, whatever lies there
-          cp_async16(vd + r * D + ((c ^ (r & 7)) * 8), vs + (ok ? r * row + c * 8 : 0), ok);   // swizzled for ldmatrix
-        }
-      }
+      const longlong2 at = table[i];
+      const int seen = static_cast<int>(at.x) & 31;
+      if (seen > 0) fetch_values<D>(smem_u32(ring) + stage * C::kStrip * 2, P.vp + at.y, row, seen, lane);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // the keys of entry i, as they lie: bytes 16 tq .. of every 64 of rows gq and gq + 8 (rows behind the
   // position hold anything; they are masked as scores)
   uint4 kx[D / 32], ky[D / 32];
+  const __nv_bfloat16* k_lane = P.kp + gq * row + tq * 8;
   auto fetch_k = [&](int i, int count) {
     if (i < count) {
-      const int2 at = table[i];
-      if ((at.y & 31) > 0) {
-        const __nv_bfloat16* ks = P.kp + at.x * P.k_stride + static_cast<int64_t>((at.y >> 16) + gq) * row + ((at.y >> 8) & 255) * D + tq * 8;
+      const long long at = table[i].x;
+      if ((at & 31) != 0) {
+        const __nv_bfloat16* ks = k_lane + (at >> 5);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           kx[c] = __ldg(reinterpret_cast<const uint4*>(ks + c * 32));
@@ -665,7 +673,8 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) page
       int page = -1;
       if (blk >= 0 && blk <= x.pos >> P.bk_shift && t0 <= x.pos) page = static_cast<int>(page_of(V, x.b, t0, kKidPagedAttn));
       const int seen = page >= 0 ? min(16, x.pos - t0 + 1) : 0;
-      table[i] = make_int2(page, (t0 & ((1 << V.shift) - 1)) << 16 | x.g << 8 | seen);
+      const int64_t in_page = (t0 & ((1 << V.shift) - 1)) * row + x.g * D;
+      table[i] = make_longlong2((page * P.k_stride + in_page) * 32 + seen, page * P.v_stride + in_page);
     }
     __syncthreads();
     int i = warp, stage = 0;
@@ -696,7 +705,7 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) page
       for (; i < stop; i += kPagedAttnWarps) {
         __syncwarp();   // every lane is done with the stage that is refilled now
         fetch_v(i + (kPagedAttnRing - 1) * kPagedAttnWarps, count, stage == 0 ? kPagedAttnRing - 1 : stage - 1);
-        const int nv = table[i].y & 31;
+        const int nv = static_cast<int>(table[i].x) & 31;
         const __nv_bfloat16* vs = ring + stage * C::kStrip;
         stage = stage + 1 == kPagedAttnRing ? 0 : stage + 1;
         if (nv == 0) {

@@ -167,16 +167,8 @@ paged_small_kernel(const __grid_constant__ PagedSmallParams P) {
     }
   };
   auto fetch_v = [&](const Place& x, int stage) {
-    if (x.seen > 0) {
-      const __nv_bfloat16* vs = P.vp + x.page * P.v_stride + x.row * krow + g * D;
-      __nv_bfloat16* vd = ring + stage * kStrip;
-#pragma unroll
-      for (int e = lane; e < 16 * (D / 8); e += 32) {
-        const int r = e / (D / 8), c = e % (D / 8);
-        const bool ok = r < x.seen;   // rows behind the position read as zeros, whatever lies there
-        cp_async16(vd + r * D + ((c ^ (r & 7)) * 8), vs + (ok ? r * krow + c * 8 : 0), ok);
-      }
-    }
+    if (x.seen > 0)
+      fetch_values<D>(smem_u32(ring) + stage * kStrip * 2, P.vp + x.page * P.v_stride + x.row * krow + g * D, krow, x.seen, lane);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
