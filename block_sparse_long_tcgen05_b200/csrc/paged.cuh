@@ -50,7 +50,8 @@ __device__ __forceinline__ uint32_t ordered_key(float m) {
 // token's block, from block nb0 on. Nothing is scanned of a sequence all of whose visible
 // blocks are selected anyway.
 //
-// Bound by the index keys' bytes. One warp takes 128 tokens of one group (32 KB at d_idx =
+// Bound by the index keys' bytes: 8 sequences of 131073 tokens (8 groups of 128 elements, 2.15 GB) take 325 us,
+// 6.6 TB/s. One warp takes 128 tokens of one group (32 KB at d_idx =
 // 128). The keys go from memory into the registers of an m16n8k16 product as they lie: lane
 // (gq, tq) loads the 16 bytes 8 tq .. 8 tq + 7 of every 32 elements of rows gq and gq + 8,
 // which serve as two steps' operands, since a dot product does not mind the order of its terms
@@ -333,9 +334,10 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
 // stand in one list, and every CTA of a single resident wave takes an equal run of it, whatever
 // the sequences' lengths; where a run ends inside a (row, group) its result is a part, and the
 // last CTA to finish one of the parts joins them, in the list's order. (One CTA for every
-// (row, group) leaves SMs idle, and clusters that share one wait for each other's places: 32 ragged
-// sequences took 47 and 63 to 87 us, against 48 here; what is left above the
-// bytes' 37 us is the chain of look-ups before the first copy and the join after the last.)
+// (row, group) leaves SMs idle: 8 sequences of 8 groups took 44 us, against 22 here. Clusters that
+// share one wait for each other's places: 32 ragged sequences took 63 to 87 us, against 48. What is
+// left above those bytes' 37 us is the chain of look-ups before the first copy, the join after the
+// last, and pieces of 256 bytes every 2 KB.)
 //
 // A warp takes every fourth strip of the run through its own ring of asynchronous copies and carries
 // its own running maximum, sum and output, so that warps meet only at the end of a (row, group).
@@ -363,8 +365,8 @@ constexpr int kPagedAttnWarps = 4;
 constexpr int kPagedAttnTable = 256;   // strips looked up at a time
 constexpr int kPagedAttnRing = 2;      // strips' values a warp has room for
 constexpr int kPagedAttnLeast = 16;    // strips of a run, where there are enough: shorter ones cost more to join than they save
-// CTAs resident on an SM. Three of 168 registers a thread: two take 7% longer (16 x 4 drafted tokens behind
-// 32K), four of 128 registers spill and take 5% longer.
+// CTAs resident on an SM. Three of 168 registers a thread; four of 128 spill (16 x 4 drafted tokens behind
+// 32K: 93 us with three, 96 with four).
 constexpr int kPagedAttnCtas(int nt) { return nt == 1 ? 3 : 2; }
 template <int D>
 struct PagedAttnCfg {

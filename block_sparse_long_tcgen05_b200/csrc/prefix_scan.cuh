@@ -7,7 +7,7 @@
 // from TMEM and stores its ordered key. Nothing else leaves the SM.
 //
 // Bound by the keys' bytes up to about 128 rows (64 rows x 131072 tokens x 8 groups: 268 MB, 41 us
-// at the copy rate, and 17 us of products at M = 128), by the products beyond. A CTA stays with one
+// at the copy rate, and 17 us of products at M = 128; takes 54), by the products beyond. A CTA stays with one
 // (row tiles, group) and takes every W-th key tile, so that CTAs of all groups stream the same
 // tokens' rows side by side.
 #pragma once
