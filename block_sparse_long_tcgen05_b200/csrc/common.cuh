@@ -30,12 +30,6 @@ enum KernelId : int {
   kKidDecodeScan = 6,
   kKidDecodeAttn = 7,
   kKidKl = 8,
-  kKidRotate = 9,
-  kKidPagedScan = 10,
-  kKidPagedTopk = 11,
-  kKidPagedAttn = 12,
-  kKidPrefixScan = 13,
-  kKidPagedSmall = 14,
 };
 
 // Device error word: low byte = first msa_status_t recorded, next byte = kernel id.

@@ -10,6 +10,7 @@
 
 #include "decode.cuh"
 #include "ptx.cuh"
+#include "step.cuh"
 
 namespace msa {
 

@@ -298,14 +298,6 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
 }
 
 // ----------------------------------------------------------------------------------
-// Kernels that follow one another (launched with programmatic stream serialisation)
-// ----------------------------------------------------------------------------------
-// Lets the next kernel's blocks start once every block of this one got here or ended.
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-// Waits until the kernel before this one is done, its writes visible (and with it those that it waited for).
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// ----------------------------------------------------------------------------------
 // Small helpers
 // ----------------------------------------------------------------------------------
 __device__ __forceinline__ float max3f(float a, float b, float c) {

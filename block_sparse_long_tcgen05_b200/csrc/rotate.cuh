@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 
 #include "ptx.cuh"
+#include "step.cuh"
 
 namespace msa {
 
