@@ -23,6 +23,8 @@ msa_status_t check_rotate_tensor(const msa_rope_tensor& t, int32_t dtype, int32_
   if (t.x == nullptr || t.y == nullptr) return fail(MSA_ERR_INVALID_ARG, "%s: NULL pointer", name);
   if (reinterpret_cast<uintptr_t>(t.x) % dtype_bytes(dtype) != 0 || reinterpret_cast<uintptr_t>(t.y) % dtype_bytes(out_dtype) != 0)
     return fail(MSA_ERR_INVALID_ARG, "%s is not aligned to its element", name);
+  if ((t.heads > 1 && t.y_head_stride == 0) || (n > 1 && t.y_token_stride == 0))
+    return fail(MSA_ERR_INVALID_ARG, "%s: several results would go to one place (a stride of 0)", name);
   return MSA_OK;
 }
 

@@ -49,7 +49,7 @@ def test_rope_refusals(lib):
         assert call(p=_with(good, **changes)) == status, changes
         assert lib.msa_last_error_detail()
     for changes, status in (({"heads": 0}, 1), ({"heads": 2000}, 1), ({"dim": 65}, 2), ({"dim": 2048}, 2), ({"dim": 0}, 2),
-                            ({"x": None}, 1), ({"y": None}, 1), ({"x": P + 1}, 1)):
+                            ({"x": None}, 1), ({"y": None}, 1), ({"x": P + 1}, 1), ({"y_head_stride": 0}, 1), ({"y_token_stride": 0}, 1)):
         assert call(t=_tensor(**changes)) == status, changes
     assert call(count=0) == 1 and call(count=5) == 1 and call(n=-1) == 1 and call(n=1 << 26) == 1
     assert call(n=0) == 0   # nothing to do, nothing enqueued
@@ -105,6 +105,7 @@ def test_append_refusals(lib):
     assert call(n=4) == 1                                   # not a multiple of the batch
     assert call(k_=_with(k, heads=3)) == 1 and call(i=_with(ki, dim=64)) == 1 and call(v=_with(k, x=None)) == 1
     assert call(q=_with(k, heads=8)) == 1                   # no destination
+    assert call(q=_with(k, y=P, y_token_stride=128)) == 1   # one destination for both heads
     assert call(n=0) == 0
 
 
