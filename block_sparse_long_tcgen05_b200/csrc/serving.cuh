@@ -47,13 +47,14 @@ template <typename TI, typename TO, int V>
 msa_status_t launch_rotate_v(RotateParams& P, cudaStream_t st) {
   int64_t blocks = 0;
   const int sms = num_sms();
+  int64_t all = 0;   // threads at a head each
+  for (int i = 0; i < P.count; ++i) all += P.n * (P.jobs[i].dim / (2 * V)) * P.jobs[i].heads;
   for (int i = 0; i < P.count; ++i) {
     RotateJob& j = P.jobs[i];
-    // One angle serves all of a thread's heads, so a thread takes up to 16 of them where that still
-    // leaves an SM its 512 resident threads, and one where tokens are few. Appending 8191 tokens takes
-    // 76 us so, and 133 us with four times the threads.
-    const int64_t per_head = P.n * (j.dim / (2 * V)) * j.heads;
-    const int64_t each = std::min<int64_t>(16, std::max<int64_t>(1, per_head / (int64_t(sms) * 2 * kRotThreads)));
+    // One angle serves all of a thread's heads, so a thread takes up to 16 of them where the call's tensors
+    // still leave an SM its 512 resident threads, and one where tokens are few. Appending 8191 tokens takes
+    // 72 us so, 76 with each tensor counted alone, and 133 with four times the threads.
+    const int64_t each = std::min<int64_t>(16, std::max<int64_t>(1, all / (int64_t(sms) * 2 * kRotThreads)));
     j.head_slots = int((j.heads + each - 1) / each);
     j.block0 = static_cast<unsigned int>(blocks);
     const int64_t threads = P.n * (j.dim / (2 * V)) * j.head_slots;
