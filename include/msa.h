@@ -22,7 +22,8 @@
  *   - Tensors are row-major and contiguous, bf16 passed as raw 16-bit storage
  *     (const void*). Every pointer is a DEVICE pointer owned by the caller, 16-byte
  *     aligned, except the input and output buffers of msa_forward_host, which are host
- *     memory. The library allocates and frees no memory; scratch memory comes from the
+ *     memory, and where the serving entry points (rotary positions, paged cache) state
+ *     types, strides and alignments of their own. The library allocates and frees no memory; scratch memory comes from the
  *     caller's workspace (size from the matching *_workspace function; 256-byte
  *     aligned base). It keeps up to three extra streams per device of its own (see
  *     msa_forward_host) and creates its events per call.
