@@ -671,7 +671,8 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) page
     for (int i = threadIdx.x; i < count; i += kThreads) {
       const StripPlace x = find_strip(P, ends, place(i));
       const int per_shift = P.bk_shift - 4;
-      const int blk = __ldg(P.block_ids + ((static_cast<int64_t>(x.b) * V.S + x.s) * P.G + x.g) * P.k + (x.at >> per_shift));
+      // (not __ldg: the Top-k may still have been writing them when this kernel began)
+      const int blk = __ldcg(P.block_ids + ((static_cast<int64_t>(x.b) * V.S + x.s) * P.G + x.g) * P.k + (x.at >> per_shift));
       const int t0 = (blk << P.bk_shift) + ((x.at & ((1 << per_shift) - 1)) << 4);
       int page = -1;
       if (blk >= 0 && blk <= x.pos >> P.bk_shift && t0 <= x.pos) page = static_cast<int>(page_of(V, x.b, t0, kKidPagedAttn));

@@ -15,7 +15,9 @@ enum ServingKernelId : int {
   kKidPagedSmall = 14,
 };
 
-// Kernels launched with programmatic stream serialisation.
+// Kernels launched with programmatic stream serialisation. What the kernel before writes is read behind
+// grid_wait, and by coherent loads: __ldg's path is for what stays as it is while a kernel runs, and this one
+// runs beside its writer.
 // Lets the next kernel's blocks start once every block of this one got here or ended.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // Waits until the kernel before this one is done, its writes visible (and with it those that it waited for).
