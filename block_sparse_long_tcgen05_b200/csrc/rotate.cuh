@@ -130,7 +130,11 @@ __global__ void __launch_bounds__(kRotThreads, 2) rotate_kernel(const __grid_con
       left = seq < P.batch ? P.cu_seqlens[seq + 1] - tok : 0;
     }
     if (tok >= P.n || seq >= P.batch) return;   // rows behind the last sequence
-    const int64_t p = static_cast<int64_t>(P.seqlens[seq]) - left;
+    const int64_t len = P.seqlens[seq];
+    const int64_t p = len - left;
+    // equal counts: an empty sequence's rows, and those before a shorter one's first token, have no token (as
+    // in the decode of the same batch)
+    if (P.cu_seqlens == nullptr && p < 0 && len >= 0) return;
     if (p < 0 || (p >> P.page_shift) >= P.max_pages) {
       record_error(MSA_ERR_DEVICE_BOUNDS, kKidRotate);
       return;

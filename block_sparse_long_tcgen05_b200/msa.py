@@ -515,7 +515,8 @@ def paged_append(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Ten
     """Writes new tokens into the cache (msa_paged_append): k, v [N, G, d], k_idx [N, G, d_idx] in bf16,
     fp16 or fp32, keys rotated by their positions on the way (freqs given; index keys by idx_freqs, or by
     freqs, unless rotate_index is False). seqlens [B] int32 counts the new tokens; cu_seqlens [B + 1] int32
-    says which rows are whose (None: N / B each); rows behind cu_seqlens[B] are padding. q [N, Hq, d] and
+    says which rows are whose (None: N / B each; rows of positions below 0, as all of an empty sequence of a
+    padded batch, then have no token); rows behind cu_seqlens[B] are padding. q [N, Hq, d] and
     q_idx [N, G, d_idx] are rotated in the same launch into q_out / q_idx_out (bf16; allocated if None,
     padding rows then undefined). Returns (q_out, q_idx_out)."""
     index, dtype, n, batch = cache.index, k.dtype, k.shape[0], seqlens.shape[0]

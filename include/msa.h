@@ -288,9 +288,11 @@ typedef struct msa_paged_append_params {
  * sequence's new tokens are its last ones: row t of sequence b has position
  * seqlens[b] - (cu_seqlens[b + 1] - t). k, v: g heads of d; k_idx: g heads of d_idx (y ignored: the
  * pages take the result); q, q_idx: any heads, y bf16. Inputs of type dtype, rounded once to bf16.
- * Rows from cu_seqlens[batch] on are padding: neither read nor written. A token outside its
- * sequence's pages, or a page outside the cache, is reported through msa_get_device_error as
- * MSA_ERR_DEVICE_BOUNDS and left out. Two tokens of a call must not share a slot. Needs no workspace. */
+ * Rows from cu_seqlens[batch] on are padding: neither read nor written. So, without cu_seqlens, are the
+ * rows whose position would be below 0, as in msa_paged_decode: all of an empty sequence (a padded batch:
+ * seqlens[b] = 0), the first ones of a sequence of fewer than n / batch tokens. Any other token outside its
+ * sequence's pages, a negative length and a page outside the cache are reported through msa_get_device_error
+ * as MSA_ERR_DEVICE_BOUNDS, the token left out. Two tokens of a call must not share a slot. Needs no workspace. */
 MSA_API msa_status_t msa_paged_append(const msa_paged_cache* cache, const msa_paged_append_params* p,
                                       const msa_rope_tensor* k, const msa_rope_tensor* v, const msa_rope_tensor* k_idx,
                                       const msa_rope_tensor* q, const msa_rope_tensor* q_idx, int64_t n, void* stream);

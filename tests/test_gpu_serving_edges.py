@@ -1,0 +1,86 @@
+"""Serving calls where they can go wrong: padded batches, equal and nearly equal scores, long runs. On the GPU,
+against fp64; tolerances as in test_gpu_serving.py unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+import serving_reference as ref
+from block_sparse_long_tcgen05_b200 import msa
+from test_gpu_serving import (_cache, _check_decode, _close_rotated, _deal, _filled, _fresh_step, _gen, _ints, _np, _randn, _step,
+                              _wider)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------ padded batches
+@pytest.mark.parametrize("each,lengths", [(1, [0, 1, 17, 0]), (4, [0, 2, 4, 33, 1])])
+def test_append_of_equal_counts_passes_over_rows_without_a_token(cuda_ok, each, lengths):
+    """Rows of positions below 0 (empty sequences, sequences of fewer tokens than rows): neither read nor
+    written, and no error."""
+    gen = _gen(40 + each)
+    B, ps, G, Hq, d, di = len(lengths), 16, 2, 8, 64, 32
+    cache = _cache(gen, 12, ps, G, d, di)
+    table, _ = _deal(gen, lengths, ps, 3, 12)
+    x = {n: _randn(gen, B * each, h, w) for n, h, w in (("k", G, d), ("v", G, d), ("k_idx", G, di), ("q", Hq, d))}
+    rows = [(r, b, p) for r, b, p in ref.new_rows(lengths, [each] * B) if p >= 0]
+    live = [r for r, _, _ in rows]
+    dead = [r for r in range(B * each) if r not in live]
+    for t in x.values():
+        t[dead] = float("nan")
+    f, _ = msa.rope_frequencies(64)
+    q_out = torch.full((B * each, Hq, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    msa.paged_append(cache, table, torch.tensor(lengths, dtype=torch.int32, device="cuda"), x["k"], x["v"], x["k_idx"], freqs=f,
+                     rotate_index=False, q=x["q"], q_out=q_out)
+    assert msa.msa_get_device_error() == 0
+    pos = np.zeros(B * each, dtype=np.int64)
+    for r, _, p in rows:
+        pos[r] = p
+    tab = table.cpu().numpy()
+    got = _np(cache.k_pages)
+    mine = torch.from_numpy(np.stack([got[tab[b, p // ps], p % ps] for _, b, p in rows]))
+    _close_rotated(mine, x["k"][live], ref.rotate(_np(x["k"]), pos, _np(f))[live], torch.bfloat16, 1.0, "k")
+    for _, b, p in rows:
+        got[tab[b, p // ps], p % ps] = np.nan
+    assert np.isnan(got).all()
+    _close_rotated(q_out[live], x["q"][live], ref.rotate(_np(x["q"]), pos, _np(f))[live], torch.bfloat16, 1.0, "q")
+    assert (q_out[dead] == 9.0).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_captured_step_of_a_padded_batch(cuda_ok, wide):
+    """Append and decode captured at a padded batch size: no error on any replay, zeros and ids of -1 for the
+    empty sequences, the others as eager calls on them give them; then a sequence takes an empty place."""
+    gen = _gen(43)
+    B, ps, G, Hq, d, di, k, max_pages = 5, 16, 2, 8, 64, 32, 4, 40
+    cache = _cache(gen, B * max_pages, ps, G, d, di, poison=False)
+    table = torch.randperm(B * max_pages, generator=gen, device="cuda").to(torch.int32).view(B, max_pages)
+    if wide:
+        table = _wider(table, ps)
+    for t in (cache.k_pages, cache.v_pages):
+        t.copy_(_randn(gen, *t.shape))
+    cache.k_idx_pages.copy_(_ints(gen, *cache.k_idx_pages.shape))
+    f, s = msa.rope_frequencies(64)
+    seq = torch.tensor([600, 0, 17, 0, 1], dtype=torch.int32, device="cuda")
+    x = _fresh_step(gen, B, G, Hq, d, di)
+    out = {"q": torch.zeros(B, Hq, d, dtype=torch.bfloat16, device="cuda"),
+           "q_idx": torch.zeros(B, G, di, dtype=torch.bfloat16, device="cuda"),
+           "o": torch.empty(B, Hq, d, dtype=torch.bfloat16, device="cuda"),
+           "ids": torch.empty(B, G, k, dtype=torch.int32, device="cuda")}
+    ws = torch.empty(msa.paged_decode_workspace(cache, B, table.shape[1], Hq, k), dtype=torch.uint8, device="cuda")
+    _step(cache, table, seq, x, f, s, k, None, out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _step(cache, table, seq, x, f, s, k, None, out, ws)
+    for lengths in ([600, 0, 17, 0, 1], [601, 0, 18, 0, 2], [0, 500, 0, 3, 0]):
+        seq.copy_(torch.tensor(lengths, dtype=torch.int32))
+        for n, t in _fresh_step(gen, B, G, Hq, d, di).items():
+            x[n].copy_(t)
+        out["o"].fill_(5.0)
+        graph.replay()
+        assert msa.msa_get_device_error() == 0, lengths
+        for b, L in enumerate(lengths):
+            if L == 0:
+                assert (out["o"][b] == 0).all() and (out["ids"][b] == -1).all()
+        _check_decode(cache, table, seq, out["q"][:, None], out["q_idx"][:, None], k, 128, None, out["o"][:, None],
+                      out["ids"][:, None])
