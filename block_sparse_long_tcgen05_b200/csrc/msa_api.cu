@@ -1438,7 +1438,9 @@ msa_status_t msa_rope(const msa_rope_params* p, const msa_rope_tensor* tensors, 
   if (!std::isfinite(p->scale)) return fail(MSA_ERR_INVALID_ARG, "scale must be finite");
   for (int i = 0; i < count; ++i) {
     static const char* const names[4] = {"tensor 0", "tensor 1", "tensor 2", "tensor 3"};
-    if ((s = check_rotate_tensor(tensors[i], p->dtype, p->dtype, p->rot, n, names[i])) != MSA_OK) return s;
+    if ((s = check_rotate_tensor(tensors[i], p->dtype, p->dtype, p->rot, n, names[i])) != MSA_OK ||
+        (s = check_in_place(tensors[i], p->dtype, p->dtype, n, names[i])) != MSA_OK)
+      return s;
   }
   if (n == 0) return MSA_OK;
   if (p->positions == nullptr) return fail(MSA_ERR_INVALID_ARG, "positions is NULL");
@@ -1501,7 +1503,9 @@ msa_status_t msa_paged_append(const msa_paged_cache* c, const msa_paged_append_p
       {q, rot, p->freqs, "q"}, {q_idx, idx_rot, p->idx_freqs, "q_idx"}};
   for (auto& x : out) {
     if (!x.t) continue;
-    if ((s = check_rotate_tensor(*x.t, p->dtype, MSA_BF16, x.rot, n, x.name)) != MSA_OK) return s;
+    if ((s = check_rotate_tensor(*x.t, p->dtype, MSA_BF16, x.rot, n, x.name)) != MSA_OK ||
+        (s = check_in_place(*x.t, p->dtype, MSA_BF16, n, x.name)) != MSA_OK)
+      return s;
     P.jobs[P.count++] = rotate_job(*x.t, x.f, x.rot);
   }
   if (n == 0) return MSA_OK;

@@ -28,6 +28,16 @@ msa_status_t check_rotate_tensor(const msa_rope_tensor& t, int32_t dtype, int32_
   return MSA_OK;
 }
 
+// A result that goes where the input lies replaces just what its thread has read only where both have the same
+// layout: element sizes and strides.
+msa_status_t check_in_place(const msa_rope_tensor& t, int32_t dtype, int32_t out_dtype, int64_t n, const char* name) {
+  if (n == 0 || t.x != t.y) return MSA_OK;
+  if (dtype_bytes(dtype) != dtype_bytes(out_dtype) || (n > 1 && t.x_token_stride != t.y_token_stride) ||
+      (t.heads > 1 && t.x_head_stride != t.y_head_stride))
+    return fail(MSA_ERR_INVALID_ARG, "%s: in place only with the same strides and element size", name);
+  return MSA_OK;
+}
+
 RotateJob rotate_job(const msa_rope_tensor& t, const double* freqs, int32_t rot) {
   RotateJob j{};
   j.src = t.x;

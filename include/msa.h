@@ -224,8 +224,9 @@ typedef enum msa_dtype_t { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP32 = 2 } msa_dtype_
 /* One tensor of heads, [n, heads, dim]: element e of head h of token t is
  * x[t * token_stride + h * head_stride + e] (strides in elements; any strides, so a slice of a
  * fused projection is taken as it lies). y is where the result goes; it may be x itself with
- * the same strides, and must not overlap it otherwise. dim: even, 2 to 1024; aligned to one
- * element at least (16-byte aligned pointers and strides take the wide path). */
+ * the same strides and element size (refused else), and must not overlap any input otherwise.
+ * dim: even, 2 to 1024; aligned to one element at least (16-byte aligned pointers and strides
+ * take the wide path). */
 typedef struct msa_rope_tensor {
   const void* x;
   void* y;

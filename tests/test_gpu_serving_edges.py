@@ -84,3 +84,28 @@ def test_captured_step_of_a_padded_batch(cuda_ok, wide):
                 assert (out["o"][b] == 0).all() and (out["ids"][b] == -1).all()
         _check_decode(cache, table, seq, out["q"][:, None], out["q_idx"][:, None], k, 128, None, out["o"][:, None],
                       out["ids"][:, None])
+
+
+# ------------------------------------------------------------------------------------ in place
+def test_queries_rotated_in_place(cuda_ok):
+    """q_out = q where both have two bytes an element (fp16 becomes bf16 where it lies); fp32 queries into a
+    bf16 view of themselves are refused."""
+    gen = _gen(44)
+    N, ps, G, Hq, d, di = 9, 16, 2, 8, 64, 32
+    f, _ = msa.rope_frequencies(64)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    seq = torch.tensor([N], dtype=torch.int32, device="cuda")
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        cache = _cache(gen, 1, ps, G, d, di)
+        k, v, ki, q = (_randn(gen, N, h, w, dtype=dtype) for h, w in ((G, d), (G, d), (G, di), (Hq, d)))
+        old = q.clone()
+        run = lambda out: msa.paged_append(cache, table, seq, k, v, ki, freqs=f, rotate_index=False, q=q, q_out=out)  # noqa: B023,E731
+        if dtype == torch.float32:
+            with pytest.raises(msa.MsaError, match="in place"):
+                run(q.view(torch.bfloat16)[:, :, :d])
+            assert torch.equal(q, old)
+            continue
+        out = q.view(torch.bfloat16)
+        run(out)
+        msa.check_device_error()
+        _close_rotated(out, old, ref.rotate(_np(old), np.arange(N), _np(f)), torch.bfloat16, 1.0, f"{dtype}")

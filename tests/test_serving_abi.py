@@ -109,6 +109,24 @@ def test_append_refusals(lib):
     assert call(n=0) == 0
 
 
+def test_results_in_place_only_where_they_replace_what_was_read(lib):
+    """y == x with other strides, or of another element size: some results would fall on inputs not read yet."""
+    good = msa.MsaRopeParams(0, 64, 0, 0, 1.0, 0, P, P)
+    for changes in ({"y_token_stride": 1024}, {"y_head_stride": 128}, {"x_token_stride": 0}, {"x_head_stride": 0}):
+        assert lib.msa_rope(good, _tensor(**changes), 1, 4, None) == 1, changes
+        assert b"place" in lib.msa_last_error_detail()
+    k = msa.MsaRopeTensor(P, None, 128, 64, 0, 0, 2, 64)
+    ki = msa.MsaRopeTensor(P, None, 64, 32, 0, 0, 2, 32)
+    c = _cache(k=2 * P, v=2 * P, k_idx=2 * P)
+    for dtype, q, q_idx in ((2, _with(k, y=P, y_token_stride=128, y_head_stride=64), None),
+                            (2, _with(k, y=P, y_token_stride=256, y_head_stride=128), None),
+                            (2, None, _with(ki, y=P, y_token_stride=64, y_head_stride=32)),
+                            (0, _with(k, y=P, y_token_stride=256, y_head_stride=64), None)):
+        p = msa.MsaPagedAppendParams(dtype, 3, 10, 0, 64, 32, 1.0, 10, P, P, None, P, P)
+        assert lib.msa_paged_append(c, p, k, k, ki, q, q_idx, 3, None) == 1
+        assert b"place" in lib.msa_last_error_detail()
+
+
 def test_frequency_schemes():
     """none: base^(-2i/rot). linear: all divided. ntk: the first pair unchanged, the last divided by the
     factor. yarn: fast pairs unchanged, slow ones divided, monotone between."""
