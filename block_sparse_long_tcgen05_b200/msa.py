@@ -368,6 +368,7 @@ _PACK_ROPE = struct.Struct("@iiiifiPP").pack
 _PACK_APPEND = struct.Struct("@iiiiiifqPPPPP").pack
 _PACK_DECODE = struct.Struct("@iiiiiiifqPPP").pack
 _fast = None
+_forward_ad = torch.autograd.forward_ad
 _current_device = getattr(torch._C, "_cuda_getDevice", None)          # absent in builds without CUDA
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -388,6 +389,17 @@ def _serving():
             out.append(fn)
         _fast = out
     return _fast
+
+
+def _no_tangent(*tensors: torch.Tensor | None) -> None:
+    if any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise ValueError("the result would carry no tangent; call this on the primals (the rotation is linear: the tangent's "
+                         "rotation is the result's tangent)")
+
+
+def _dual() -> bool:
+    """Whether tensors may carry tangents: a dual_level is open."""
+    return getattr(_forward_ad, "_current_level", 0) >= 0
 
 
 def _heads(x: torch.Tensor, name: str, n: int, index: int, dtype, y: torch.Tensor | None = None, y_dtype=None) -> bytes:
@@ -421,6 +433,8 @@ def _freqs(t: torch.Tensor, name: str, index: int) -> tuple[int, int]:
     shape = t.shape
     if t.dtype is not torch.float64 or len(shape) != 1 or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float64 [rot / 2] on device {index}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: frequencies get no gradient here; detach them")
     return t.data_ptr(), 2 * shape[0]
 
 
@@ -451,6 +465,8 @@ def rope(x, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = Fa
         raise ValueError("expected CUDA tensors")
     if dtype not in _DTYPES:
         raise ValueError(f"rope takes bfloat16, float16 and float32, not {dtype}")
+    if _dual():
+        _no_tangent(freqs, *xs)
     if positions.dtype != torch.int64 and positions.dtype != torch.int32:
         raise ValueError("positions must be int32 or int64")
     if out is None:
@@ -522,6 +538,8 @@ def paged_append(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Ten
     index, dtype, n, batch = cache.index, k.dtype, k.shape[0], seqlens.shape[0]
     if dtype not in _DTYPES:
         raise ValueError(f"paged_append takes bfloat16, float16 and float32, not {dtype}")
+    if _dual():
+        _no_tangent(k, v, k_idx, q, q_idx, freqs, idx_freqs)
     table, columns, stride = _table(page_table, index, batch)
     if (q is None and q_out is not None) or (q_idx is None and q_idx_out is not None):
         raise ValueError("q_out or q_idx_out without its input")
@@ -566,8 +584,11 @@ def paged_decode(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Ten
         raise ValueError(f"q must be [B, Hq, {cache.d}] or [B, tokens, Hq, {cache.d}]")
     batch, hq = shape[0], shape[-2]
     S = 1 if len(shape) == 3 else shape[1]
-    if torch.is_grad_enabled() and (q.requires_grad or q_idx.requires_grad):
+    kp, vp = cache.k_pages, cache.v_pages
+    if torch.is_grad_enabled() and (q.requires_grad or q_idx.requires_grad or kp.requires_grad or vp.requires_grad):
         raise ValueError("the result would carry no gradient; call this under torch.no_grad()")
+    if _dual():
+        _no_tangent(q, q_idx, kp, vp)
     table, columns, stride = _table(page_table, index, batch)
     lens = _small(seqlens, "seqlens", index, torch.int32, (batch,))
     bf16, lead = torch.bfloat16, shape[:-2]

@@ -109,3 +109,38 @@ def test_queries_rotated_in_place(cuda_ok):
         run(out)
         msa.check_device_error()
         _close_rotated(out, old, ref.rotate(_np(old), np.arange(N), _np(f)), torch.bfloat16, 1.0, f"{dtype}")
+
+
+# ------------------------------------------------------------------------------------ derivatives
+def test_derivatives_that_would_be_dropped_are_refused(cuda_ok):
+    """A tangent of any input (forward mode), and a gradient of the frequencies or the pages."""
+    import torch.autograd.forward_ad as fw
+    gen = _gen(45)
+    cache, table, _, seq, q, qi = _filled(gen, [200, 100], 16, 2, 64, 32, 1, 8, 13)
+    f, _ = msa.rope_frequencies(64)
+    pos = torch.arange(2, device="cuda")
+    k, v, ki = _randn(gen, 2, 2, 64), _randn(gen, 2, 2, 64), _randn(gen, 2, 2, 32)
+    append = lambda **c: msa.paged_append(cache, table, seq, **{"k": k, "v": v, "k_idx": ki, "freqs": f, "rotate_index": False, **c})  # noqa: E731
+    with fw.dual_level():
+        dual = lambda t: fw.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for call in (lambda: msa.rope(dual(k), pos, f), lambda: msa.rope((k, dual(v)), pos, f), lambda: msa.rope(k, pos, dual(f)),
+                     lambda: append(k=dual(k)), lambda: append(q=dual(k)), lambda: append(freqs=dual(f)),
+                     lambda: msa.paged_decode(cache, table, seq, dual(q), qi, 4),
+                     lambda: msa.paged_decode(cache, table, seq, q, dual(qi), 4)):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+        msa.rope(k, pos, f)   # nothing here carries one
+        append()
+        msa.paged_decode(cache, table, seq, q, qi, 4)
+    learnt = f.clone().requires_grad_()
+    for call in (lambda: msa.rope(k, pos, learnt), lambda: append(freqs=learnt)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad():
+            call()
+    grown = msa.PagedCache(cache.k_pages.clone().requires_grad_(), cache.v_pages, cache.k_idx_pages)
+    with pytest.raises(ValueError, match="gradient"):
+        msa.paged_decode(grown, table, seq, q, qi, 4)
+    with torch.no_grad():
+        assert torch.equal(msa.paged_decode(grown, table, seq, q, qi, 4), msa.paged_decode(cache, table, seq, q, qi, 4))
+    msa.check_device_error()
