@@ -565,8 +565,8 @@ def paged_decode_workspace(cache: PagedCache, batch: int, max_pages: int, hq: in
     """Bytes of workspace of paged_decode for page tables of max_pages columns."""
     p = MsaPagedDecodeParams(hq, batch, n_new, bk, topk, max_pages, 0, 0.0, max_pages, None, None, None)
     need = load_library().msa_paged_decode_workspace(cache.c, p)
-    if need == 0:
-        raise MsaError(2, load_library().msa_last_error_detail().decode())
+    if need == 0:   # the call itself, refused for the same sizes, says which kind of refusal it is
+        _check(load_library().msa_paged_decode(cache.c, p, None, None, None, None, None, 0, None))
     return need
 
 
@@ -608,8 +608,8 @@ def paged_decode(cache: PagedCache, page_table: torch.Tensor, seqlens: torch.Ten
     need = cache.workspaces.get(sizes)
     if need is None:
         need = fns[2](cache.address, p)
-        if need == 0:
-            raise MsaError(2, load_library().msa_last_error_detail().decode())
+        if need == 0:   # refused: by the call itself with its status
+            _check(fns[3](cache.address, p, qp, qip, idp, op, None, 0, None))
         cache.workspaces[sizes] = need
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

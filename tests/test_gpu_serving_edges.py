@@ -144,3 +144,19 @@ def test_derivatives_that_would_be_dropped_are_refused(cuda_ok):
     with torch.no_grad():
         assert torch.equal(msa.paged_decode(grown, table, seq, q, qi, 4), msa.paged_decode(cache, table, seq, q, qi, 4))
     msa.check_device_error()
+
+
+# ------------------------------------------------------------------------------------ refusals
+def test_refusals_carry_the_librarys_status(cuda_ok):
+    """A bad argument is MSA_ERR_INVALID_ARG (1), a valid shape that is not implemented MSA_ERR_UNSUPPORTED (2)."""
+    gen = _gen(46)
+    cache, table, _, seq, q, qi = _filled(gen, [200, 100], 16, 2, 64, 32, 1, 8, 13)
+    run = lambda q=q, k=4, **more: msa.paged_decode(cache, table, seq, q, qi, k, **more)  # noqa: E731
+    for call, status in ((lambda: run(scale=-1.0), 1), (lambda: run(scale=float("nan")), 1), (lambda: run(q=q[:, :, :7].contiguous()), 1),
+                         (lambda: run(bk=48), 2), (lambda: run(k=33), 2),
+                         (lambda: msa.paged_decode_workspace(cache, 2, 13, 7, 4), 1),
+                         (lambda: msa.paged_decode_workspace(cache, 2, 0, 8, 4), 1),
+                         (lambda: msa.paged_decode_workspace(cache, 2, 13, 8, 40), 2)):
+        with pytest.raises(msa.MsaError) as e:
+            call()
+        assert e.value.status == status and len(str(e.value)) > len("MSA_ERR_INVALID_ARG: ")
