@@ -493,13 +493,15 @@ class PagedCache:
         if k_pages.dim() != 4 or k_idx_pages.dim() != 4 or v_pages.shape != k_pages.shape \
                 or k_idx_pages.shape[:3] != k_pages.shape[:3]:
             raise ValueError("pages must be [pages, page_size, G, dim] of one geometry")
+        if 0 in k_pages.shape or 0 in k_idx_pages.shape:
+            raise ValueError("a cache has at least one page, and pages at least one row")
         self.device = k_pages.device
         if self.device.type != "cuda":
             raise ValueError("expected CUDA tensors")
         for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_idx_pages, "k_idx_pages")):
             if t.dtype != torch.bfloat16 or t.device != self.device:
                 raise ValueError(f"{name} must be bfloat16 on {self.device}")
-            if t.numel() and not t[0].is_contiguous():
+            if not t[0].is_contiguous():
                 raise ValueError(f"{name}: a page must be contiguous")
         self.k_pages, self.v_pages, self.k_idx_pages = k_pages, v_pages, k_idx_pages
         self.num_pages, self.page_size, self.G, self.d = k_pages.shape

@@ -127,6 +127,15 @@ def test_results_in_place_only_where_they_replace_what_was_read(lib):
         assert b"place" in lib.msa_last_error_detail()
 
 
+def test_a_pool_without_pages_is_refused(lib):
+    pool = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16)  # noqa: E731
+    for shape in ((0, 16, 2, 64), (4, 0, 2, 64), (4, 16, 0, 64)):
+        with pytest.raises(ValueError, match="at least one"):
+            msa.PagedCache(pool(*shape), pool(*shape), pool(*shape[:3], 32))
+    with pytest.raises(ValueError, match="CUDA"):
+        msa.PagedCache(pool(4, 16, 2, 64), pool(4, 16, 2, 64), pool(4, 16, 2, 32))
+
+
 def test_frequency_schemes():
     """none: base^(-2i/rot). linear: all divided. ntk: the first pair unchanged, the last divided by the
     factor. yarn: fast pairs unchanged, slow ones divided, monotone between."""
