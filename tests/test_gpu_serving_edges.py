@@ -160,3 +160,130 @@ def test_refusals_carry_the_librarys_status(cuda_ok):
         with pytest.raises(msa.MsaError) as e:
             call()
         assert e.value.status == status and len(str(e.value)) > len("MSA_ERR_INVALID_ARG: ")
+
+
+# ------------------------------------------------------------------------------------ selections
+def _poured(gen, lengths, ps, G, d, di, S, Hq, shared, keys, queries):
+    """A cache that holds the sequences (shared: pages that all of them begin with), NaN in every other row;
+    keys(n) gives n tokens' index keys, queries the index queries."""
+    table, common = _deal(gen, lengths, ps, max(-(-L // ps) for L in lengths) + 1, sum(-(-L // ps) for L in lengths) + shared + 2, shared)
+    cache = _cache(gen, sum(-(-L // ps) for L in lengths) + shared + 2, ps, G, d, di)
+    for b, L in enumerate(lengths):
+        first = shared if b else 0   # the shared pages with the first sequence
+        n = L - first * ps
+        if n <= 0:
+            continue
+        pages = table[b, first:-(-L // ps)].long()
+        slots = (pages[:, None] * ps + torch.arange(ps, device="cuda")).flatten()[:n]
+        for pool, new in ((cache.k_pages, _randn(gen, n, G, d)), (cache.v_pages, _randn(gen, n, G, d)), (cache.k_idx_pages, keys(n))):
+            pool.view(-1, *pool.shape[2:])[slots] = new
+    q = _randn(gen, len(lengths), S, Hq, d)
+    return cache, table, common, torch.tensor(lengths, dtype=torch.int32, device="cuda"), q, queries
+
+
+REAL = [
+    # lengths, S, Hq, G, d, di, k, bk, ps, shared pages
+    ([1500, 0, 700, 33], 1, 8, 2, 64, 32, 4, 32, 16, 0),
+    ([9000, 2500], 2, 16, 4, 128, 128, 16, 128, 64, 0),
+    ([40000], 1, 2, 1, 64, 64, 16, 32, 128, 0),                        # two chunks of Top-k
+    ([2300, 2100, 2049] * 10, 1, 8, 4, 64, 128, 5, 128, 64, 32),       # the prefix scored once for 30 rows
+    ([4200, 4097, 0, 5000] * 6, 8, 8, 2, 64, 128, 8, 64, 32, 128),     # for 192 rows
+]
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("lengths,S,Hq,G,d,di,k,bk,ps,shared", REAL)
+def test_decode_of_real_index_inputs(cuda_ok, lengths, S, Hq, G, d, di, k, bk, ps, shared, wide):
+    """Scores that are not exact: products of bf16 are exact in fp32 and a score is di of them added in some
+    order, each addition off by at most 2^-23 of the terms' sum of absolutes, so a block's maximum is off by at
+    most E = di 2^-23 max sum |q k|. Every chosen block's score reaches every other one's within the two E; the
+    attention over the chosen blocks is held to fp64 as always."""
+    gen = _gen(50 + k + bk)
+    queries = _randn(gen, len(lengths), S, G, di)
+    cache, table, common, seq, q, qi = _poured(gen, lengths, ps, G, d, di, S, Hq, shared, lambda n: _randn(gen, n, G, di), queries)
+    full = table
+    if wide:
+        table = full = _wider(table, ps)
+    if shared:
+        table = table.clone()
+        table[:, :shared] = -1
+    ids = torch.full((len(lengths), S, G, k), -9, dtype=torch.int32, device="cuda")
+    o = msa.paged_decode(cache, table, seq, q, qi, k, bk=bk, prefix_pages=common if shared else None, block_ids=ids)
+    msa.check_device_error()
+    tab, chosen, got, R = full.cpu().numpy(), ids.cpu().numpy(), _np(o), Hq // G
+    qn, qin = _np(q), _np(qi)
+    pools = [_np(t) for t in (cache.k_pages, cache.v_pages, cache.k_idx_pages)]
+    for b, L in enumerate(lengths):
+        pages = tab[b][:-(-L // ps)]
+        kk, vv, ki = (t[pages].reshape(-1, G, t.shape[3])[:L] for t in pools)
+        for s in range(S):
+            p = L - S + s
+            for g in range(G):
+                row = chosen[b, s, g]
+                if p < 0:
+                    assert (row == -1).all() and (got[b, s] == 0).all()
+                    continue
+                local = p // bk
+                take = row[row >= 0]
+                assert len(take) == min(k, local + 1) and (np.diff(take) > 0).all() and take[-1] == local
+                assert (row[len(take):] == -1).all()
+                terms = ki[:local * bk, g] * qin[b, s, g]
+                score = terms.sum(-1).reshape(local, bk).max(1)
+                off = di * 2.0 ** -23 * np.abs(terms).sum(-1).reshape(local, bk).max(1)
+                inside = np.zeros(local, dtype=bool)
+                inside[take[:-1]] = True
+                if inside.any() and not inside.all():
+                    assert (score + off)[inside].min() >= (score - off)[~inside].max()
+                tok = (take[:, None] * bk + np.arange(bk)).reshape(-1)
+                tok = tok[tok <= p]
+                z = qn[b, s, g * R:(g + 1) * R] @ kk[tok, g].T / np.sqrt(d)
+                w = np.exp(z - z.max(-1, keepdims=True))
+                w /= w.sum(-1, keepdims=True)
+                want, weight = w @ vv[tok, g], w @ np.abs(vv[tok, g])
+                err = np.abs(got[b, s, g * R:(g + 1) * R] - want)
+                assert (err <= (2.0 ** -8 + 1e-4) * weight + 2.0 ** -8 * (np.abs(want) + 2.0 ** -8 * weight)).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("k", [2, 6, 7, 16, 32])
+@pytest.mark.parametrize("length,low,high", [
+    (2000, 0, 0), (5000, 0, 0), (40000, 0, 0), (2000, 0, 2), (5000, -3, 0), (40000, 0, 1), (40000, -1, 0), (70000, 0, 3)])
+def test_decode_of_few_different_scores(cuda_ok, length, low, high, k, wide):
+    """Blocks of 32 with scores from a few whole numbers, so that tens to thousands are equal: the lower blocks
+    first, wherever the chunks of the Top-k begin."""
+    gen = _gen(60 + k)
+    G, di = 2, 32
+
+    def keys(n):
+        x = torch.zeros(n, G, di, dtype=torch.bfloat16, device="cuda")
+        x[..., 0] = torch.randint(low, high + 1, (n // 32 + 1, G), generator=gen, device="cuda").repeat_interleave(32, 0)[:n].to(x.dtype)
+        x[..., 0] += -0.0
+        return x
+
+    one = torch.zeros(1, 1, G, di, dtype=torch.bfloat16, device="cuda")
+    one[..., 0] = 1.0
+    cache, table, _, seq, q, qi = _poured(gen, [length], 128, G, 64, di, 1, 4, 0, keys, one)
+    if wide:
+        table = _wider(table, 128)
+    ids = torch.empty(1, 1, G, k, dtype=torch.int32, device="cuda")
+    o = msa.paged_decode(cache, table, seq, q, qi, k, bk=32, block_ids=ids)
+    msa.check_device_error()
+    _check_decode(cache, table, seq, q, qi, k, 32, None, o, ids)
+
+
+@pytest.mark.parametrize("B,G,k,d", [(64, 8, 32, 64), (200, 4, 16, 128)])
+def test_decode_behind_a_prefix_in_long_runs(cuda_ok, B, G, k, d):
+    """More strips a CTA than one table holds (the first), and just fewer (the second), behind a prefix."""
+    gen = _gen(70 + B)
+    ps, di, shared = 64, 32, 80
+    own = torch.randint(1, 300, (B,), generator=torch.Generator().manual_seed(5)).tolist()
+    lengths = [shared * ps + n for n in own]
+    cache, table, common, seq, q, qi = _poured(gen, lengths, ps, G, d, di, 1, G, shared, lambda n: _ints(gen, n, G, di),
+                                               _ints(gen, B, 1, G, di))
+    full = table.clone()
+    table[:, :shared] = -1
+    ids = torch.empty(B, 1, G, k, dtype=torch.int32, device="cuda")
+    o = msa.paged_decode(cache, table, seq, q, qi, k, prefix_pages=common, block_ids=ids)
+    msa.check_device_error()
+    _check_decode(cache, table, seq, q, qi, k, 128, None, o, ids, full)
+    assert torch.equal(o, msa.paged_decode(cache, table, seq, q, qi, k, prefix_pages=common))

@@ -154,3 +154,18 @@ def test_frequency_schemes():
                 dict(rot=8, scaling="yarn", factor=2.0, beta_fast=1.0, beta_slow=2.0)):
         with pytest.raises(ValueError):
             msa.rope_frequencies(device="cpu", **bad)
+
+
+@pytest.mark.parametrize("rot,base,trained,factor", [(128, 10000.0, 4096, 8.0), (64, 500000.0, 8192, 32.0), (32, 10000.0, 2048, 2.0)])
+def test_yarn_pairs_between(rot, base, trained, factor):
+    """The ramp's ends are the last pair of at least 32 turns in the trained length and the first of at most
+    one; between them a pair's frequency goes from its own to the stretched one in equal steps."""
+    own = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    turns = [trained * f / (2.0 * math.pi) for f in own]
+    lo = max(i for i, t in enumerate(turns) if t >= 32.0)
+    hi = min((i for i, t in enumerate(turns) if t <= 1.0), default=None)
+    assert hi is not None and hi - lo > 2   # there are pairs between
+    got, _ = msa.rope_frequencies(rot, base=base, scaling="yarn", factor=factor, trained_length=trained, device="cpu")
+    for i, f in enumerate(own):
+        part = min(1.0, max(0.0, (i - lo) / (hi - lo)))
+        assert abs(float(got[i]) / (f * (1.0 - part) + f / factor * part) - 1.0) < 1e-14, i
