@@ -8,8 +8,11 @@
 //
 // Angles: fp32 cannot hold p * f at positions of long contexts (2^20 * 2^-24 is 1/16 rad), so
 // the frequency is taken as a 64-bit fixed-point fraction of a turn and multiplied with the
-// position modulo 2^64: whole turns drop out exactly, and what remains is off by at most
-// |p| * 2^-54 turns. Its upper 32 bits go to sincospif (error below 2^-25 half turns).
+// position modulo 2^64: whole turns drop out exactly. The turns a position, f / (2 pi) in fp64, are
+// off by at most |f| 2^-55 (half a step of the product, and of 1 / (2 pi), which are 2^-53 and 2^-53.9
+// of it), where f is negative by 2^-54 more (the step up from below 0), and the fixed point by 2^-65: the
+// angle by |p| times that, 2^-55 turns a position for the usual f <= 1. Its upper 32 bits go to sincospif:
+// cutting the others off is 2^-31 half turns at most, rounding what is left to fp32 2^-25.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -92,8 +92,11 @@ bool rotate_fits(const RotateParams& P, int V) {
   return true;
 }
 
-// The widest access that fits, 16 bytes at best: the 32K prompt of 64 + 8 heads takes 191 us with
-// 16-byte accesses and 1516 element by element.
+// The widest access that fits all tensors of the call, 16 bytes at best, else two elements, else one; the
+// tensor that fits least decides for the call. The 32K prompt of 64 + 8 heads in bf16 takes 191-196 us with
+// 16-byte accesses, 300 two elements at a time and 393 element by element (in fp32, whose 16 bytes are four
+// elements, 362, 394 and 459); appending 8191 tokens with index keys that rotate 128 or 32 elements 77-79 us, 24
+// or 20 elements 116, 14 elements 161.
 template <typename TI, typename TO>
 msa_status_t launch_rotate(RotateParams& P, cudaStream_t st) {
   constexpr int W = 16 / sizeof(TI);
@@ -252,6 +255,7 @@ msa_status_t launch_prefix_scan(const CUtensorMap& tq, const CUtensorMap& tk, Pr
   msa_status_t s;
   if ((s = smem_limit(limit, prefix_scan_kernel<DI, RT>, C::kSmemBytes)) != MSA_OK) return s;
   const int sms = num_sms();
+  // (a pair's share of the SMs is rounded down: between half as many pairs as SMs and all of them, the rest idle)
   P.pairs = (P.rows + RT * 128 - 1) / (RT * 128) * P.G;
   P.workers = std::max(1, std::min(sms / P.pairs, P.tiles));
   const int grid = P.workers > 1 ? P.workers * P.pairs : std::min(sms, P.pairs);
@@ -288,7 +292,9 @@ msa_status_t launch_paged_attn(const PagedAttnParams& P, cudaStream_t st) {
 
 // One launch for the whole decode. Wanted where the clusters of all (row, group)s are resident at once (they
 // gain 30 to 45% there; at twice as many the three kernels are as fast, at four times faster) and a cluster
-// scans the longest sequence in about the time that two more launches take: 16384 tokens (8 groups of 128
+// scans the longest sequence in about the time that two more launches take. Lengths are known on the device
+// alone, so the longest sequence is taken to be what the page table has room for: one of 700 tokens takes 7.7 us
+// under a table of 44 pages of 16 and 14.2 under one of 1025. 16384 tokens (8 groups of 128
 // index elements: 28 us against 30; at 30000 tokens 51 against 34), 256 blocks (500 blocks of 32 tokens:
 // 23 against 17). `done`: whether it was launched.
 template <int D, int NT, int DI>

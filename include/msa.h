@@ -225,8 +225,10 @@ typedef enum msa_dtype_t { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP32 = 2 } msa_dtype_
  * x[t * token_stride + h * head_stride + e] (strides in elements; any strides, so a slice of a
  * fused projection is taken as it lies). y is where the result goes; it may be x itself with
  * the same strides and element size (refused else), and must not overlap any input otherwise.
- * dim: even, 2 to 1024; aligned to one element at least (16-byte aligned pointers and strides
- * take the wide path). */
+ * dim: even, 2 to 1024; aligned to one element at least. A call moves 16 bytes at a time where, with
+ * V the elements of 16 bytes, every tensor's pointers are 16-byte aligned, its strides multiples
+ * of V, rot / 2 a multiple of V and dim - rot of 2 V; else two elements or one at a time, which
+ * takes 1.5 to 2 times as long: one tensor that does not fit slows all of its call. */
 typedef struct msa_rope_tensor {
   const void* x;
   void* y;
@@ -319,6 +321,11 @@ typedef struct msa_paged_decode_params {
  * seqlens[b] = 0) gets zeros and ids of -1. Lengths above the table's and pages outside the cache are
  * reported as MSA_ERR_DEVICE_BOUNDS; the outputs of such sequences are then undefined (nothing is read
  * or written out of range). Cache rows behind a sequence's end may hold anything.
+ * o and block_ids_out must not overlap any input. Scores are sums in fp32 whose order depends on the kernel
+ * that the sizes choose (with a shared prefix on the batch, too): blocks whose scores differ by less than such sums'
+ * rounding may be selected in place of one another. Softmax weights are rounded to bf16 for their product with
+ * the values (their sum is not). Few and short sequences are decoded in one launch, where the page table has room
+ * for at most 16384 tokens and 256 blocks: give it the columns that the sequences may need.
  * Only enqueues launches whose grids depend on the parameters alone: may be captured into a CUDA graph.
  * Calls that may run at the same time, replays among them, need a workspace each. */
 MSA_API size_t msa_paged_decode_workspace(const msa_paged_cache* cache, const msa_paged_decode_params* p);
