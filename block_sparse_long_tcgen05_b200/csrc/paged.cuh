@@ -349,8 +349,11 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
 // The products are m16n8k16, transposed so that the group's R <= 16 heads are the columns (too few
 // for tcgen05's rows; one or two tiles of 8): S^T = K Q^T has the strip's tokens as rows, O^T += V^T P^T
 // the output's elements. The probabilities go from the first one's accumulators into the second's
-// operand through a transposition in registers (movmatrix), rounded to bf16 (off by at most 2^-8 of
-// each weight, what the output is rounded to as well); maximum, sum and output stay in fp32.
+// operand through a transposition in registers (movmatrix), as two bf16 numbers each, the weight rounded and
+// what that left out, also rounded: off by at most 2^-16 of each weight. (One, off by 2^-8, put the outputs
+// 2.1e-3 from the 64-bit ones where their own rounding is 1.7e-3; the second product costs the 16 x 4 drafted
+// tokens behind 32K 3 us, 85 to 88, one short sequence 0.1 us, the other calls nothing.) Maximum, sum and
+// output stay in fp32.
 // ------------------------------------------------------------------------------------
 struct PagedAttnParams {
   PageView view;
@@ -435,10 +438,11 @@ __device__ __forceinline__ void strip_scores(const uint4 (&kx)[D / 32], const ui
 }
 
 // The strip's softmax against the running maximum and sum (m, l: heads 8 t + 2 tq and the next; the sum is
-// of this lane's tokens), its weights P^T as an operand; nv: tokens that count.
+// of this lane's tokens), its weights P^T as operands: what they are in bf16 and, behind that, what is left;
+// nv: tokens that count.
 template <int D, int NT>
 __device__ __forceinline__ void strip_softmax(const float (&sc)[NT][2][4], int nv, float scale_log2, int gq, float (&m)[NT][2],
-                                              float (&l)[NT][2], float (&o)[NT][D / 16][4], uint32_t (&pf)[NT][2]) {
+                                              float (&l)[NT][2], float (&o)[NT][D / 16][4], uint32_t (&pf)[NT][4]) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float x[4], top[2] = {m[t][0], m[t][1]};
@@ -463,8 +467,11 @@ __device__ __forceinline__ void strip_softmax(const float (&sc)[NT][2][4], int n
       x[y] = exp2f(x[y] - top[y & 1]);
       l[t][y & 1] += x[y];
     }
-    pf[t][0] = transpose_8x8(pack_bf16x2(x[0], x[1]));
-    pf[t][1] = transpose_8x8(pack_bf16x2(x[2], x[3]));
+    const uint32_t hi0 = pack_bf16x2(x[0], x[1]), hi1 = pack_bf16x2(x[2], x[3]);
+    pf[t][0] = transpose_8x8(hi0);
+    pf[t][1] = transpose_8x8(hi1);
+    pf[t][2] = transpose_8x8(pack_bf16x2(x[0] - __uint_as_float(hi0 << 16), x[1] - __uint_as_float(hi0 & 0xffff0000u)));
+    pf[t][3] = transpose_8x8(pack_bf16x2(x[2] - __uint_as_float(hi1 << 16), x[3] - __uint_as_float(hi1 & 0xffff0000u)));
     if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
 #pragma unroll
       for (int n = 0; n < D / 16; ++n)
@@ -474,16 +481,19 @@ __device__ __forceinline__ void strip_softmax(const float (&sc)[NT][2][4], int n
   }
 }
 
-// O^T += V^T P^T: the strip's values in shared memory, 16-byte pieces c of row r at c ^ (r % 8).
+// O^T += V^T P^T, for both parts of P: the strip's values in shared memory, 16-byte pieces c of row r at c ^ (r % 8).
 template <int D, int NT>
-__device__ __forceinline__ void strip_values(const __nv_bfloat16* vs, int lane, const uint32_t (&pf)[NT][2], float (&o)[NT][D / 16][4]) {
+__device__ __forceinline__ void strip_values(const __nv_bfloat16* vs, int lane, const uint32_t (&pf)[NT][4], float (&o)[NT][D / 16][4]) {
   const int vr = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
   for (int n = 0; n < D / 16; ++n) {
     uint32_t af[4];
     ldsm_x4_trans(af, vs + vr * D + (((n * 2 + ((lane >> 3) & 1)) ^ (vr & 7)) * 8));
 #pragma unroll
-    for (int t = 0; t < NT; ++t) mma_16816(o[t][n], af, pf[t]);
+    for (int t = 0; t < NT; ++t) {
+      mma_16816(o[t][n], af, {pf[t][0], pf[t][1]});
+      mma_16816(o[t][n], af, {pf[t][2], pf[t][3]});
+    }
   }
 }
 
@@ -719,7 +729,7 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) page
         float sc[NT][2][4];
         strip_scores<D, NT>(kx, ky, qf, sc);
         fetch_k(i + kPagedAttnWarps, count);   // under this strip's softmax and values
-        uint32_t pf[NT][2];
+        uint32_t pf[NT][4];
         strip_softmax<D, NT>(sc, nv, P.scale_log2, gq, m, l, o, pf);
         asm volatile("cp.async.wait_group %0;" ::"n"(kPagedAttnRing - 1) : "memory");
         __syncwarp();

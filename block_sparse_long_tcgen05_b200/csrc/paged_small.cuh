@@ -193,7 +193,7 @@ paged_small_kernel(const __grid_constant__ PagedSmallParams P) {
       float sc[NT][2][4];
       strip_scores<D, NT>(kx, ky, qf, sc);
       fetch_k(next);
-      uint32_t pf[NT][2];
+      uint32_t pf[NT][4];
       strip_softmax<D, NT>(sc, cur.seen, P.scale_log2, gq, m, l, o, pf);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();

@@ -323,8 +323,7 @@ typedef struct msa_paged_decode_params {
  * or written out of range). Cache rows behind a sequence's end may hold anything.
  * o and block_ids_out must not overlap any input. Scores are sums in fp32 whose order depends on the kernel
  * that the sizes choose (with a shared prefix on the batch, too): blocks whose scores differ by less than such sums'
- * rounding may be selected in place of one another. Softmax weights are rounded to bf16 for their product with
- * the values (their sum is not). Few and short sequences are decoded in one launch, where the page table has room
+ * rounding may be selected in place of one another. Few and short sequences are decoded in one launch, where the page table has room
  * for at most 16384 tokens and 256 blocks: give it the columns that the sequences may need.
  * Only enqueues launches whose grids depend on the parameters alone: may be captured into a CUDA graph.
  * Calls that may run at the same time, replays among them, need a workspace each. */

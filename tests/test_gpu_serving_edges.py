@@ -287,3 +287,28 @@ def test_decode_behind_a_prefix_in_long_runs(cuda_ok, B, G, k, d):
     msa.check_device_error()
     _check_decode(cache, table, seq, q, qi, k, 128, None, o, ids, full)
     assert torch.equal(o, msa.paged_decode(cache, table, seq, q, qi, k, prefix_pages=common))
+
+
+# ------------------------------------------------------------------------------------ precision
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("lengths,S,Hq,G,d,k,bk", [
+    ([700, 3, 0, 129, 1], 1, 8, 2, 64, 4, 128), ([2500, 2, 1111], 4, 16, 1, 128, 5, 128), ([1300, 97], 1, 8, 8, 64, 8, 32),
+    ([9000] * 12, 1, 64, 8, 128, 16, 128)])
+def test_decode_outputs_are_off_by_their_own_rounding(cuda_ok, lengths, S, Hq, G, d, k, bk, wide):
+    """Weights enter their product as a bf16 number and the bf16 number nearest to the rest: off by at most 2^-8
+    times 2^-8 of each, 2^-16 W in all (W: sum of weight * |v|); logits as in test_gpu_serving.py, 1e-4 W; then
+    the output's own rounding, 2^-8 of the value. Weights in one bf16 number, off by up to 2^-8 each, do not pass."""
+    gen = _gen(80 + k)
+    ps, di = 16, 32
+    cache, table, _, seq, q, qi = _poured(gen, lengths, ps, G, d, di, S, Hq, 0, lambda n: _ints(gen, n, G, di),
+                                          _ints(gen, len(lengths), S, G, di))
+    if wide:
+        table = _wider(table, ps)
+    o = msa.paged_decode(cache, table, seq, q, qi, k, bk=bk)
+    msa.check_device_error()
+    want, _, weight = ref.decode(_np(q), _np(qi), _np(cache.k_pages), _np(cache.v_pages), _np(cache.k_idx_pages),
+                                 table.cpu().numpy(), seq.cpu().numpy(), k, bk)
+    before = (2.0 ** -16 + 1e-4) * weight
+    err = np.abs(_np(o) - want)
+    bad = ~(err <= before + 2.0 ** -8 * (np.abs(want) + before))
+    assert not bad.any(), f"{bad.sum()} of {bad.size} out of tolerance, max err {err.max():.3e}"
