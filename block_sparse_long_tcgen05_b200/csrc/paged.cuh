@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kPagedAttnWarps * 32, kPagedAttnCtas(NT)) page
   // Behind a shared prefix a run of one table takes the unit that it begins first, then the whole ones, then
   // the end of the one that another run began: so all CTAs go through low blocks first and high ones last,
   // and what rows select in common is still in L2 (64 sequences behind 128K tokens: 157 us, in the list's
-  // order 164). Runs of several tables keep the list's order: batches of more than 110 rows with 8 groups and 16
+  // order 164). Runs of several tables keep the list's order: batches of more than 111 rows with 8 groups and 16
   // blocks of 128 each, 55 with 32 blocks (a row's attention takes 1.12 us at 104 rows and 1.22 at 112).
   // place(i): where entry i of the table lies.
   const bool turned = V.prefix_pages > 0 && end - begin <= kPagedAttnTable;
