@@ -349,8 +349,9 @@ __global__ void __launch_bounds__(128) paged_topk_kernel(const __grid_constant__
 // The products are m16n8k16, transposed so that the group's R <= 16 heads are the columns (too few
 // for tcgen05's rows; one or two tiles of 8): S^T = K Q^T has the strip's tokens as rows, O^T += V^T P^T
 // the output's elements. The probabilities go from the first one's accumulators into the second's
-// operand through a transposition in registers (movmatrix), as two bf16 numbers each, the weight rounded and
-// what that left out, also rounded: off by at most 2^-16 of each weight. (One, off by 2^-8, put the outputs
+// operand through a transposition in registers (movmatrix), as two bf16 numbers each, the weight cut off and
+// what that left (less than 2^-7 of it), rounded: off by at most 2^-15 + 2^-20 of each weight. Neither is negative
+// or, of a positive weight, zero, so an infinite value gives an infinite output. (One number, off by 2^-8, put the outputs
 // 2.1e-3 from the 64-bit ones where their own rounding is 1.7e-3; the second product costs the 16 x 4 drafted
 // tokens behind 32K 3 us, 85 to 88, one short sequence 0.1 us, the other calls nothing.) Maximum, sum and
 // output stay in fp32.
@@ -438,7 +439,7 @@ __device__ __forceinline__ void strip_scores(const uint4 (&kx)[D / 32], const ui
 }
 
 // The strip's softmax against the running maximum and sum (m, l: heads 8 t + 2 tq and the next; the sum is
-// of this lane's tokens), its weights P^T as operands: what they are in bf16 and, behind that, what is left;
+// of this lane's tokens), its weights P^T as operands: cut off to bf16 and, behind that, what is left;
 // nv: tokens that count.
 template <int D, int NT>
 __device__ __forceinline__ void strip_softmax(const float (&sc)[NT][2][4], int nv, float scale_log2, int gq, float (&m)[NT][2],
@@ -467,11 +468,15 @@ __device__ __forceinline__ void strip_softmax(const float (&sc)[NT][2][4], int n
       x[y] = exp2f(x[y] - top[y & 1]);
       l[t][y & 1] += x[y];
     }
-    const uint32_t hi0 = pack_bf16x2(x[0], x[1]), hi1 = pack_bf16x2(x[2], x[3]);
-    pf[t][0] = transpose_8x8(hi0);
-    pf[t][1] = transpose_8x8(hi1);
-    pf[t][2] = transpose_8x8(pack_bf16x2(x[0] - __uint_as_float(hi0 << 16), x[1] - __uint_as_float(hi0 & 0xffff0000u)));
-    pf[t][3] = transpose_8x8(pack_bf16x2(x[2] - __uint_as_float(hi1 << 16), x[3] - __uint_as_float(hi1 & 0xffff0000u)));
+    float rest[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y)   // a little more than the rest, so that no positive weight has a zero or negative one
+      rest[y] = fmaf(x[y], 1.0f + 0x1p-20f, -__uint_as_float(__float_as_uint(x[y]) & 0xffff0000u));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      pf[t][h] = transpose_8x8(__byte_perm(__float_as_uint(x[2 * h]), __float_as_uint(x[2 * h + 1]), 0x7632));   // the upper halves
+      pf[t][2 + h] = transpose_8x8(pack_bf16x2(rest[2 * h], rest[2 * h + 1]));
+    }
     if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
 #pragma unroll
       for (int n = 0; n < D / 16; ++n)

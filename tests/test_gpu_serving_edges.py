@@ -295,9 +295,10 @@ def test_decode_behind_a_prefix_in_long_runs(cuda_ok, B, G, k, d):
     ([700, 3, 0, 129, 1], 1, 8, 2, 64, 4, 128), ([2500, 2, 1111], 4, 16, 1, 128, 5, 128), ([1300, 97], 1, 8, 8, 64, 8, 32),
     ([9000] * 12, 1, 64, 8, 128, 16, 128)])
 def test_decode_outputs_are_off_by_their_own_rounding(cuda_ok, lengths, S, Hq, G, d, k, bk, wide):
-    """Weights enter their product as a bf16 number and the bf16 number nearest to the rest: off by at most 2^-8
-    times 2^-8 of each, 2^-16 W in all (W: sum of weight * |v|); logits as in test_gpu_serving.py, 1e-4 W; then
-    the output's own rounding, 2^-8 of the value. Weights in one bf16 number, off by up to 2^-8 each, do not pass."""
+    """Weights enter their product cut off to bf16 (8 bits: less than 2^-7 of each is left) and, for the rest and
+    2^-20 of the weight, the bf16 number nearest to that: off by at most 2^-8 times 2^-7, and 2^-20, of each, in all
+    (2^-15 + 2^-20) W (W: sum of weight * |v|); logits as in test_gpu_serving.py, 1e-4 W; then the output's own
+    rounding, 2^-8 of the value. Weights in one bf16 number, off by up to 2^-8 each, do not pass."""
     gen = _gen(80 + k)
     ps, di = 16, 32
     cache, table, _, seq, q, qi = _poured(gen, lengths, ps, G, d, di, S, Hq, 0, lambda n: _ints(gen, n, G, di),
@@ -308,7 +309,30 @@ def test_decode_outputs_are_off_by_their_own_rounding(cuda_ok, lengths, S, Hq, G
     msa.check_device_error()
     want, _, weight = ref.decode(_np(q), _np(qi), _np(cache.k_pages), _np(cache.v_pages), _np(cache.k_idx_pages),
                                  table.cpu().numpy(), seq.cpu().numpy(), k, bk)
-    before = (2.0 ** -16 + 1e-4) * weight
+    before = (2.0 ** -15 + 2.0 ** -20 + 1e-4) * weight
     err = np.abs(_np(o) - want)
     bad = ~(err <= before + 2.0 ** -8 * (np.abs(want) + before))
     assert not bad.any(), f"{bad.sum()} of {bad.size} out of tolerance, max err {err.max():.3e}"
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_infinite_values_give_infinite_outputs(cuda_ok, wide):
+    """A token's values of +inf or -inf, whatever its weight, 1 and powers of two among them: that infinity, as the
+    formula has it; both signs in one place, or a NaN: NaN; the other elements as without them."""
+    gen = _gen(90)
+    lengths, ps, G, Hq, d, di, k = [1, 200, 700], 16, 2, 8, 64, 32, 8
+    cache, table, _, seq, q, qi = _poured(gen, lengths, ps, G, d, di, 1, Hq, 0, lambda n: _ints(gen, n, G, di), _ints(gen, 3, 1, G, di))
+    q *= 0.25
+    if wide:
+        table = _wider(table, ps)
+    plain = msa.paged_decode(cache, table, seq, q, qi, k)
+    want = plain.clone().view(3, G, Hq // G, d)
+    inf = float("inf")
+    for b, t, g, e, v, out in ((0, 0, 0, 3, inf, inf), (0, 0, 1, 63, -inf, -inf), (1, 0, 0, 0, inf, inf), (1, 199, 1, 17, -inf, -inf),
+                               (2, 690, 0, 5, inf, inf), (2, 645, 1, 6, -inf, -inf), (1, 50, 0, 9, inf, inf), (1, 51, 0, 9, -inf, inf - inf),
+                               (2, 699, 1, 40, inf - inf, inf - inf)):
+        cache.v_pages[int(table[b, t // ps]), t % ps, g, e] = v
+        want[b, g, :, e] = out
+    got = msa.paged_decode(cache, table, seq, q, qi, k).view(3, G, Hq // G, d)
+    msa.check_device_error()
+    torch.testing.assert_close(got, want, rtol=0, atol=0, equal_nan=True)
